@@ -252,12 +252,13 @@ def _own_attn(s):
         s["shape"] = lf.LfShape.make(c["B"], c["H"], c["D"], c["F"], c["frames"], c["sink"], c["recent"], c["cur"])
         fwd = lf.lf_attn_split_plan(s["shape"], s["cap"])[2]
         s["ws"] = torch.empty(fwd, dtype=torch.uint8, device="cuda") if fwd else None
+        s["out_lo"] = torch.empty_like(s["out"])
         s["ws_bwd"] = torch.empty(lf.lf_attn_bwd_workspace(s["shape"]), dtype=torch.uint8, device="cuda")
     sh = s["shape"]
     lf.lf_block_sparse_attn_lse(sh, s["q"], s["k"], s["v"], s["lists"], s["count"], s["cap"], 0.0, s["out"], s["lse"],
-                                workspace=s["ws"])
+                                workspace=s["ws"], out_lo=s["out_lo"])
     lf.lf_block_sparse_attn_bwd(sh, s["q"], s["k"], s["v"], s["out"], s["dout"], s["lse"], s["lists"], s["count"],
-                                s["cap"], 0.0, s["dq"], s["dk"], s["dv"], s["ws_bwd"])
+                                s["cap"], 0.0, s["dq"], s["dk"], s["dv"], s["ws_bwd"], out_lo=s["out_lo"])
     return {n: s[n] for n in ("out", "lse", "dq", "dk", "dv")}
 
 
