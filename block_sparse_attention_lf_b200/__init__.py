@@ -44,6 +44,8 @@ __all__ = [
     "lf_block_sparse_attn", "lf_block_sparse_attn_ws", "lf_attn_split_plan", "lf_cag_budget",
     "lf_blocks_for_sparsity", "lf_frames_selected", "lf_list_capacity", "lf_get_device_error",
     "lf_status_string", "lf_version", "HSACall",
+    "lf_block_sparse_attn_lse", "lf_block_sparse_attn_bwd", "lf_attn_bwd_workspace",
+    "RopePlan", "lf_rope", "NormGateShape", "lf_norm_gate", "lf_norm_gate_bwd", "lf_norm_gate_bwd_workspace",
     "ABI_FUNCTIONS", "shard_units", "shard_shape", "unit_view",
 ]
 
@@ -54,6 +56,8 @@ ABI_FUNCTIONS = (
     "lf_block_sparse_attn_fp8",
     "lf_block_sparse_attn", "lf_block_sparse_attn_ws", "lf_attn_split_plan", "lf_block_sparse_attn_static",
     "lf_cag_budget", "lf_blocks_for_sparsity", "lf_get_device_error", "lf_status_string", "lf_version",
+    "lf_block_sparse_attn_lse", "lf_attn_bwd_workspace", "lf_block_sparse_attn_bwd",
+    "lf_rope_plan_init", "lf_rope", "lf_norm_gate", "lf_norm_gate_bwd_workspace", "lf_norm_gate_bwd",
 )
 
 LF_OK = 0
@@ -107,6 +111,79 @@ class LfShape(ctypes.Structure):
         return self.n_frames * self.frame_tokens
 
 
+class RopePlan(ctypes.Structure):
+    """Mirror of ``lf_rope_plan``: a head's rotary frequencies (``make``), kept by the caller."""
+
+    _fields_ = [
+        ("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+        ("n_axes", ctypes.c_int32), ("axis_dims", ctypes.c_int32 * 3), ("amplitude", ctypes.c_float),
+        ("turns", ctypes.c_double * 128),
+    ]
+
+    LAYOUTS = {"interleaved": 0, "half": 1}
+    SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+    @classmethod
+    def make(cls, head_dim: int, rot_dim: Optional[int] = None, layout: str = "interleaved",
+             axis_dims: Optional[Sequence[int]] = None, base: float = 10000.0, scaling: str = "none",
+             factor: float = 1.0, original_length: float = 0.0, beta_fast: float = 32.0,
+             beta_slow: float = 1.0) -> "RopePlan":
+        """``axis_dims``: rotated dimensions of each position axis (one axis of ``rot_dim`` by default);
+        ``scaling`` stretches axis 0 by ``factor`` (``original_length``: trained positions, for yarn)."""
+        if layout not in cls.LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(cls.LAYOUTS)}")
+        if scaling not in cls.SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(cls.SCALINGS)}")
+        rot = head_dim if rot_dim is None else rot_dim
+        dims = [rot] if axis_dims is None else [int(d) for d in axis_dims]
+        plan = cls()
+        arr = (ctypes.c_int32 * max(len(dims), 1))(*dims)
+        _check(_lib.lf_rope_plan_init(ctypes.byref(plan), head_dim, rot, cls.LAYOUTS[layout], len(dims),
+                                      ctypes.cast(arr, ctypes.c_void_p), float(base), cls.SCALINGS[scaling],
+                                      float(factor), float(original_length), float(beta_fast), float(beta_slow)),
+               "RopePlan.make")
+        return plan
+
+
+class _RopeIo(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("x_stride", ctypes.c_int64 * 3),
+                ("out_stride", ctypes.c_int64 * 3), ("heads", ctypes.c_int32), ("rotate", ctypes.c_int32)]
+
+
+class NormGateShape(ctypes.Structure):
+    """Mirror of ``lf_norm_gate_shape``."""
+
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("rows_per_group", ctypes.c_int64), ("dim", ctypes.c_int32),
+        ("x_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("pre_norm", ctypes.c_int32),
+        ("post_norm", ctypes.c_int32), ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float),
+    ]
+
+    NORMS = {"none": 0, "rms": 1, "layer": 2}
+
+    @classmethod
+    def make(cls, rows: int, dim: int, rows_per_group: Optional[int] = None, x_dtype=None, y_dtype=None,
+             pre: str = "layer", post: str = "none", eps: float = 1e-6, residual_scale: float = 1.0) -> "NormGateShape":
+        """``rows_per_group``: consecutive rows that share gate, scale and shift (default: all rows);
+        dtypes default to bf16."""
+        if pre not in cls.NORMS or post not in cls.NORMS:
+            raise ValueError(f"norms must be one of {sorted(cls.NORMS)}")
+        bf = _bf16()
+        return cls(rows, max(rows, 1) if rows_per_group is None else rows_per_group, dim, _dtype_code(x_dtype or bf),
+                   _dtype_code(y_dtype or bf), cls.NORMS[pre], cls.NORMS[post], eps, residual_scale)
+
+    @property
+    def groups(self) -> int:
+        return -(-self.rows // self.rows_per_group)
+
+
+_NORM_VECTORS = ("gate", "scale", "shift", "pre_w", "pre_b", "post_w", "post_b")
+
+
+class _NormVectors(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in _NORM_VECTORS]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -136,6 +213,14 @@ def _load() -> ctypes.CDLL:
         "lf_cag_budget": ([I32, P, P, F64, F64, I32, P, P], I32),
         "lf_blocks_for_sparsity": ([F64, I32, I32, I32], I32),
         "lf_get_device_error": ([ctypes.POINTER(I32)], I32),
+        "lf_block_sparse_attn_lse": ([S, P, P, P, P, P, I32, F32, P, P, P, I32, P, ctypes.c_int64, P], I32),
+        "lf_attn_bwd_workspace": ([S], ctypes.c_int64),
+        "lf_block_sparse_attn_bwd": ([S, P, P, P, P, P, P, P, P, P, I32, F32, P, P, P, P, ctypes.c_int64, P], I32),
+        "lf_rope_plan_init": ([P, I32, I32, I32, I32, P, F64, I32, F64, F64, F64, F64], I32),
+        "lf_rope": ([P, I32, I32, I32, P, ctypes.c_int64, P, I32, I32, P], I32),
+        "lf_norm_gate": ([P, P, P, P, P, P, P], I32),
+        "lf_norm_gate_bwd_workspace": ([P], ctypes.c_int64),
+        "lf_norm_gate_bwd": ([P, P, P, P, P, P, P, P, P, P, ctypes.c_int64, P], I32),
         "lf_status_string": ([I32], ctypes.c_char_p),
         "lf_version": ([], ctypes.c_char_p),
     }
@@ -178,6 +263,29 @@ def _stream(stream):
 def _bf16():
     import torch
     return torch.bfloat16
+
+
+def _dtype_code(dtype) -> int:
+    import torch
+    codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    if dtype not in codes:
+        raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+    return codes[dtype]
+
+
+def _sized_ptr(t, dtype, shape, device, name: str) -> int:
+    """Address of a contiguous CUDA tensor of exactly this dtype and shape on ``device``."""
+    _dev_ptr(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device.index != device:
+        raise ValueError(f"{name} must be on the current device (cuda:{device}), got {t.device}")
+    return t.data_ptr()
+
+
+def _device() -> int:
+    import torch
+    return torch.cuda.current_device()
 
 
 def lf_version() -> str:
@@ -370,6 +478,168 @@ def lf_block_sparse_attn_fp8(shape: LfShape, q8, k8, q_scale, k_scale, v, block_
            "lf_block_sparse_attn_fp8")
 
 
+def _attn_args(shape: LfShape, dev: int, q, k, v, block_list, block_count, list_cap: int):
+    import torch
+    bf, i32 = torch.bfloat16, torch.int32
+    B, H, D = shape.batch, shape.heads, shape.head_dim
+    kv = (B, H, shape.kv_stride or shape.Lkv, D)
+    return (_sized_ptr(q, bf, (B, H, shape.Lq, D), dev, "q"), _sized_ptr(k, bf, kv, dev, "k"),
+            _sized_ptr(v, bf, kv, dev, "v"),
+            _sized_ptr(block_list, i32, (B, H, shape.Rq, list_cap), dev, "block_list"),
+            _sized_ptr(block_count, i32, (B, H, shape.Rq), dev, "block_count"))
+
+
+def lf_block_sparse_attn_lse(shape: LfShape, q, k, v, block_list, block_count, list_cap: int, softmax_scale: float,
+                             out, lse, workspace=None, tail_pieces: int = 0, stream=None, out_lo=None) -> None:
+    """lf_block_sparse_attn_ws that also writes each row's log-sum-exp (fp32 [B,H,Lq]; -inf for an empty list)
+    and, for the gradient, ``out_lo`` (like out): out + out_lo is the row under the rounded softmax weights."""
+    import torch
+    dev = _device()
+    qp, kp, vp, lp, cp = _attn_args(shape, dev, q, k, v, block_list, block_count, list_cap)
+    ws = _sized_ptr(workspace, torch.uint8, workspace.shape, dev, "workspace") if workspace is not None else None
+    ws_bytes = workspace.numel() if workspace is not None else 0
+    _check(_lib.lf_block_sparse_attn_lse(
+        ctypes.byref(shape), qp, kp, vp, lp, cp, list_cap, float(softmax_scale),
+        _sized_ptr(out, torch.bfloat16, q.shape, dev, "out"),
+        None if out_lo is None else _sized_ptr(out_lo, torch.bfloat16, q.shape, dev, "out_lo"),
+        _sized_ptr(lse, torch.float32, q.shape[:3], dev, "lse"), int(tail_pieces), ws, ws_bytes,
+        _stream(stream)), "lf_block_sparse_attn_lse")
+
+
+def lf_attn_bwd_workspace(shape: LfShape) -> int:
+    """Bytes of the workspace of lf_block_sparse_attn_bwd."""
+    n = _lib.lf_attn_bwd_workspace(ctypes.byref(shape))
+    if n < 0:
+        raise LfError(3, "lf_attn_bwd_workspace")
+    return n
+
+
+def lf_block_sparse_attn_bwd(shape: LfShape, q, k, v, out, dout, lse, block_list, block_count, list_cap: int,
+                             softmax_scale: float, dq, dk, dv, workspace, stream=None, out_lo=None) -> None:
+    """Gradient of the attention in q, k and v over the same lists (out, out_lo and lse from
+    lf_block_sparse_attn_lse; out_lo may be left out at some loss of accuracy); ``workspace``: a uint8 device tensor of lf_attn_bwd_workspace(shape) bytes."""
+    import torch
+    bf, dev = torch.bfloat16, _device()
+    qp, kp, vp, lp, cp = _attn_args(shape, dev, q, k, v, block_list, block_count, list_cap)
+    _check(_lib.lf_block_sparse_attn_bwd(
+        ctypes.byref(shape), qp, kp, vp, _sized_ptr(out, bf, q.shape, dev, "out"),
+        None if out_lo is None else _sized_ptr(out_lo, bf, q.shape, dev, "out_lo"),
+        _sized_ptr(dout, bf, q.shape, dev, "dout"), _sized_ptr(lse, torch.float32, q.shape[:3], dev, "lse"), lp, cp,
+        list_cap, float(softmax_scale), _sized_ptr(dq, bf, q.shape, dev, "dq"),
+        _sized_ptr(dk, bf, k.shape, dev, "dk"), _sized_ptr(dv, bf, k.shape, dev, "dv"),
+        _sized_ptr(workspace, torch.uint8, workspace.shape, dev, "workspace"), workspace.numel(), _stream(stream)),
+        "lf_block_sparse_attn_bwd")
+
+
+def lf_rope(plan: RopePlan, xs: Sequence, outs: Sequence, positions, rotate: Optional[Sequence[bool]] = None,
+            backward: bool = False, stream=None) -> None:
+    """Rotary positions of up to three tensors in one launch.
+
+    ``xs`` and ``outs``: [batch, heads, tokens, head_dim] views of any strides (the last one 1) and
+    one dtype (fp32, bf16, fp16), e.g. slices of a fused token-major projection and slots of the
+    call's head-major tensors; an output may be its own input. ``positions``: int32
+    [tokens, n_axes] or [batch, tokens, n_axes]. ``rotate[i]`` False copies tensor i. ``backward``:
+    xs are gradients of the outputs, outs receive the gradients of the inputs."""
+    import torch
+    n = len(xs)
+    if len(outs) != n or not 1 <= n <= 3:
+        raise ValueError("lf_rope takes one to three tensors and as many outputs")
+    dev, dtype = _device(), xs[0].dtype
+    B, _, T, D = xs[0].shape
+    if D != plan.head_dim:
+        raise ValueError(f"tensors have head_dim {D}, the plan {plan.head_dim}")
+    io = (_RopeIo * n)()
+    for i in range(n):
+        x, o = xs[i], outs[i]
+        for t, name in ((x, "x"), (o, "out")):
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+            if t.device.index != dev:
+                raise ValueError(f"{name} must be on the current device (cuda:{dev}), got {t.device}")
+            if t.dtype != dtype:
+                raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        shape, xst, ost = x.shape, x.stride(), o.stride()
+        if len(shape) != 4 or shape[0] != B or shape[2] != T or shape[3] != D or o.shape != shape:
+            raise ValueError("every tensor and its output must be [batch, heads, tokens, head_dim] of the same sizes")
+        if xst[3] != 1 or ost[3] != 1:
+            raise ValueError("the last dimension must have stride 1")
+        e = io[i]
+        e.x, e.out, e.heads, e.rotate = x.data_ptr(), o.data_ptr(), shape[1], 1 if rotate is None or rotate[i] else 0
+        e.x_stride[:], e.out_stride[:] = xst[:3], ost[:3]
+    shared = positions.dim() == 2
+    _sized_ptr(positions, torch.int32, (T, plan.n_axes) if shared else (B, T, plan.n_axes), dev, "positions")
+    _check(_lib.lf_rope(ctypes.byref(plan), B, T, _dtype_code(dtype), positions.data_ptr(),
+                        0 if shared else T * plan.n_axes, io, n, 1 if backward else 0, _stream(stream)), "lf_rope")
+
+
+def _norm_vectors(shape: NormGateShape, dev: int, tensors: dict) -> _NormVectors:
+    import torch
+    v = _NormVectors()
+    for name, t in tensors.items():
+        if t is not None:
+            want = (shape.groups, shape.dim) if name in ("gate", "scale", "shift") else (shape.dim,)
+            setattr(v, name, _sized_ptr(t, torch.float32, want, dev, name))
+    return v
+
+
+def _norm_dtypes(shape: NormGateShape):
+    import torch
+    types = (torch.float32, torch.bfloat16, torch.float16)
+    return types[shape.x_dtype], types[shape.y_dtype]
+
+
+def lf_norm_gate(shape: NormGateShape, x, y, r, h, gate=None, scale=None, shift=None, pre_w=None, pre_b=None,
+                 post_w=None, post_b=None, stream=None) -> None:
+    """r = residual_scale x + gate post(y); h = pre(r) (1 + scale) + shift, in one pass over [rows, dim]
+    (``y``, ``r`` or ``h`` may be None). gate, scale, shift: fp32 [groups, dim]; weights and biases fp32 [dim]."""
+    dev = _device()
+    xd, yd = _norm_dtypes(shape)
+    want = (shape.rows, shape.dim)
+
+    def opt(t, dtype, name):
+        return None if t is None else _sized_ptr(t, dtype, want, dev, name)
+
+    v = _norm_vectors(shape, dev, dict(gate=gate, scale=scale, shift=shift, pre_w=pre_w, pre_b=pre_b, post_w=post_w,
+                                       post_b=post_b))
+    _check(_lib.lf_norm_gate(ctypes.byref(shape), ctypes.byref(v), _sized_ptr(x, xd, want, dev, "x"), opt(y, yd, "y"),
+                             opt(r, xd, "r"), opt(h, yd, "h"), _stream(stream)), "lf_norm_gate")
+
+
+def lf_norm_gate_bwd_workspace(shape: NormGateShape) -> int:
+    """Bytes of the workspace of lf_norm_gate_bwd."""
+    n = _lib.lf_norm_gate_bwd_workspace(ctypes.byref(shape))
+    if n < 0:
+        raise LfError(3, "lf_norm_gate_bwd_workspace")
+    return n
+
+
+def lf_norm_gate_bwd(shape: NormGateShape, x, y, dr, dh, dx, dy, grads: dict, workspace, gate=None, scale=None,
+                     shift=None, pre_w=None, pre_b=None, post_w=None, post_b=None, stream=None) -> None:
+    """Gradients of lf_norm_gate from its own inputs. ``dr`` / ``dh``: gradients of r and h (None: none);
+    ``dx`` / ``dy``: outputs (None: not wanted); ``grads``: fp32 outputs by vector name (gate, scale, shift,
+    pre_w, ...), shaped as the vectors; ``workspace``: a uint8 device tensor of
+    lf_norm_gate_bwd_workspace(shape) bytes."""
+    import torch
+    dev = _device()
+    xd, yd = _norm_dtypes(shape)
+    want = (shape.rows, shape.dim)
+
+    def opt(t, dtype, name):
+        return None if t is None else _sized_ptr(t, dtype, want, dev, name)
+
+    for name in grads:
+        if name not in _NORM_VECTORS:
+            raise ValueError(f"unknown gradient {name}")
+    v = _norm_vectors(shape, dev, dict(gate=gate, scale=scale, shift=shift, pre_w=pre_w, pre_b=pre_b, post_w=post_w,
+                                       post_b=post_b))
+    g = _norm_vectors(shape, dev, grads)
+    _check(_lib.lf_norm_gate_bwd(
+        ctypes.byref(shape), ctypes.byref(v), _sized_ptr(x, xd, want, dev, "x"), opt(y, yd, "y"), opt(dr, xd, "dr"),
+        opt(dh, yd, "dh"), opt(dx, xd, "dx"), opt(dy, yd, "dy"), ctypes.byref(g),
+        _sized_ptr(workspace, torch.uint8, workspace.shape, dev, "workspace"), workspace.numel(), _stream(stream)),
+        "lf_norm_gate_bwd")
+
+
 def lf_attn_split_plan(shape: LfShape, list_cap: int, sm: int = 0) -> Tuple[int, int, int]:
     """(tail query blocks, pieces per list, workspace bytes) of the automatic split."""
     t, p, b = ctypes.c_int32(0), ctypes.c_int32(0), ctypes.c_int64(0)
@@ -420,11 +690,14 @@ class HSACall:
     ``topk_frames`` / ``topk_blocks`` as in the C ABI. ``tail_pieces`` selects
     the attention's split of the last, partial wave (0: automatic plan for the
     current device, 1: none, k >= 2: k pieces); the workspace it needs is
-    allocated here.
+    allocated here. ``train=True`` keeps each row's log-sum-exp, so that
+    ``backward`` can give the gradients of the last call. ``load`` and
+    ``load_bwd`` bring a chunk's fused projection into the call's tensors with
+    rotary positions applied, and the gradients back.
     """
 
     def __init__(self, shape: LfShape, chunk_index: int, topk_frames: int, topk_blocks: int,
-                 device="cuda", softmax_scale: float = 0.0, tail_pieces: int = 0):
+                 device="cuda", softmax_scale: float = 0.0, tail_pieces: int = 0, train: bool = False):
         import torch
         self.shape, self.chunk_index = shape, chunk_index
         self.topk_frames, self.topk_blocks = topk_frames, topk_blocks
@@ -462,6 +735,9 @@ class HSACall:
         ws_bytes = tail * pieces * 64 * (D + 2) * 4
         self.workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device) if ws_bytes else None
         self.split = (tail, pieces) if ws_bytes else (0, 0)
+        self.lse = torch.empty(s.batch, s.heads, s.Lq, dtype=f32, device=device) if train else None
+        self.out_lo = torch.empty_like(self.buf.out) if train else None
+        self.bwd_workspace = torch.empty(lf_attn_bwd_workspace(s), dtype=torch.uint8, device=device) if train else None
         # kernels enqueued per call: pool, selection (both levels), attention (+ the merge of a split)
         self.launches_per_call = 3 + (1 if ws_bytes else 0)
 
@@ -474,8 +750,36 @@ class HSACall:
         lf_select_mask(self.shape, self.chunk_index, self.topk_frames, self.topk_blocks, b.q_pool, b.k_frame,
                        b.k_pool, b.frame_sel, b.block_list, b.block_count, b.list_cap, stream)
 
+    def load(self, plan: RopePlan, qkv, positions, q, k, v, stream=None):
+        """The chunk's projection ``qkv`` [batch, Lq, 3, heads, head_dim] (bf16) into ``q`` and the
+        current-chunk frames of ``k`` and ``v``, q and k rotated (one launch, lf_rope)."""
+        xs, (kc, vc) = qkv.permute(2, 0, 3, 1, 4).unbind(0), self._current(k, v)
+        lf_rope(plan, xs, (q, kc, vc), positions, rotate=(True, True, False), stream=stream)
+
+    def load_bwd(self, plan: RopePlan, dq, dk, dv, positions, dqkv, stream=None):
+        """Gradient of ``load``: ``dqkv`` from ``dq`` and the current-chunk frames of ``dk`` and ``dv``."""
+        outs, (kc, vc) = dqkv.permute(2, 0, 3, 1, 4).unbind(0), self._current(dk, dv)
+        lf_rope(plan, (dq, kc, vc), outs, positions, rotate=(True, True, False), backward=True, stream=stream)
+
+    def _current(self, *ts):
+        s = self.shape
+        return [t[:, :, s.Lkv - s.Lq:s.Lkv] for t in ts]
+
+    def backward(self, q, k, v, dout, dq, dk, dv, stream=None):
+        """Gradients of the last call's output in q, k and v (``train=True``; the selected blocks are constants)."""
+        if self.lse is None:
+            raise ValueError("HSACall.backward needs train=True")
+        b = self.buf
+        lf_block_sparse_attn_bwd(self.shape, q, k, v, b.out, dout, self.lse, b.block_list, b.block_count, b.list_cap,
+                                 self.softmax_scale, dq, dk, dv, self.bwd_workspace, stream, out_lo=self.out_lo)
+
     def attend(self, q, k, v, stream=None):
         b = self.buf
+        if self.lse is not None:
+            lf_block_sparse_attn_lse(self.shape, q, k, v, b.block_list, b.block_count, b.list_cap,
+                                     self.softmax_scale, b.out, self.lse, self.workspace, self.tail_pieces, stream,
+                                     out_lo=self.out_lo)
+            return
         lf_block_sparse_attn_ws(self.shape, q, k, v, b.block_list, b.block_count, b.list_cap,
                                 self.softmax_scale, b.out, self.workspace, self.tail_pieces, stream)
 

@@ -2,8 +2,11 @@
 // argument validation, TMA descriptor encoding, kernel launches, the
 // Chunk-Aware Growth solver and the per-device error word.
 #include "lf_hsa.h"
+#include "lf_attn_bwd.h"
 #include "lf_device.cuh"
 #include "lf_internal.h"
+#include "lf_norm.h"
+#include "lf_rope.h"
 
 #include <algorithm>
 #include <cmath>
@@ -132,6 +135,18 @@ lf_status sm_count(int* out)
     return LF_OK;
 }
 
+// The current device must be the one the kernels are compiled for (sm_100).
+lf_status check_device()
+{
+    int dev = 0, major = 0, minor = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return LF_ERR_NO_DEVICE;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+        return LF_ERR_NO_DEVICE;
+    if (major != 10 || minor != 0) return LF_ERR_NO_DEVICE;
+    return LF_OK;
+}
+
 // ---- TMA descriptors ------------------------------------------------------
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 {
@@ -196,6 +211,49 @@ bool encode_blocks_il(CUtensorMap* m, const void* base, long long rows, int grou
     return r == CUDA_SUCCESS;
 }
 
+// 4-D bf16 view [head][frame][token of the frame][D] with a box of one 64-element panel of
+// 64 tokens of one frame and 128-byte swizzle: tokens past the frame's end (a partial
+// block), and a frame index past the last one, read as zeros instead of a neighbour's rows.
+bool encode_frames(CUtensorMap* m, const void* base, const Derived& d, int frames, long long head_rows)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t row = static_cast<cuuint64_t>(d.D) * 2u;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d.D), static_cast<cuuint64_t>(d.F),
+                                static_cast<cuuint64_t>(frames), static_cast<cuuint64_t>(d.B) * d.H};
+    const cuuint64_t strides[3] = {row, row * d.F, row * static_cast<cuuint64_t>(head_rows)};
+    const cuuint32_t box[4] = {64u, 64u, 1u, 1u};
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+// Workspace of the attention's gradient: each row's delta, and for each KV block the query
+// blocks that list it (ascending) with their number.
+struct BwdPlan {
+    long long delta, row_count, row_list, bytes;
+};
+
+BwdPlan bwd_plan(const Derived& d)
+{
+    const long long BH = static_cast<long long>(d.B) * d.H;
+    auto up = [](long long n) { return (n + 255) / 256 * 256; };
+    BwdPlan p;
+    p.delta = 0;
+    p.row_count = up(BH * d.Lq * 4);
+    p.row_list = p.row_count + up(BH * d.Nkv * 4);
+    p.bytes = p.row_list + up(BH * d.Nkv * d.Rq * 4);
+    return p;
+}
+
+// lf_block_sparse_attn_ws and, where lse is not null, lf_block_sparse_attn_lse.
+lf_status attn_bf16(const lf_hsa_shape* shape, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                    const int32_t* block_list, const int32_t* block_count, int32_t list_cap, float softmax_scale,
+                    uint16_t* out, uint16_t* out_lo, float* lse, int32_t tail_pieces, void* workspace,
+                    int64_t workspace_bytes, void* stream);
+
 }  // namespace
 
 extern "C" {
@@ -217,7 +275,7 @@ const char* lf_status_string(lf_status s)
     case LF_ERR_ARG: return "invalid argument";
     case LF_ERR_LIST: return "block id or count out of range";
     case LF_ERR_NO_DEVICE: return "no usable CUDA device";
-    case LF_ERR_SCRATCH: return "the call needs more than the library's static scratch array";
+    case LF_ERR_SCRATCH: return "the call needs more than the library's static scratch array or the given workspace";
     }
     return "unknown status";
 }
@@ -424,6 +482,97 @@ lf_status lf_block_sparse_attn_ws(const lf_hsa_shape* shape, const uint16_t* q, 
                                   float softmax_scale, uint16_t* out, int32_t tail_pieces, void* workspace,
                                   int64_t workspace_bytes, void* stream)
 {
+    return attn_bf16(shape, q, k, v, block_list, block_count, list_cap, softmax_scale, out, nullptr, nullptr, tail_pieces,
+                     workspace, workspace_bytes, stream);
+}
+
+lf_status lf_block_sparse_attn_lse(const lf_hsa_shape* shape, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                                   const int32_t* block_list, const int32_t* block_count, int32_t list_cap,
+                                   float softmax_scale, uint16_t* out, uint16_t* out_lo, float* lse,
+                                   int32_t tail_pieces, void* workspace, int64_t workspace_bytes, void* stream)
+{
+    if (!lse) return LF_ERR_NULL;
+    if (!aligned16(lse) || !aligned16(out_lo)) return LF_ERR_ALIGN;
+    return attn_bf16(shape, q, k, v, block_list, block_count, list_cap, softmax_scale, out, out_lo, lse, tail_pieces,
+                     workspace, workspace_bytes, stream);
+}
+
+int64_t lf_attn_bwd_workspace(const lf_hsa_shape* shape)
+{
+    Derived d;
+    if (check_shape(shape, &d) != LF_OK) return -1;
+    return bwd_plan(d).bytes;
+}
+
+lf_status lf_block_sparse_attn_bwd(const lf_hsa_shape* shape, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                                   const uint16_t* out, const uint16_t* out_lo, const uint16_t* dout,
+                                   const float* lse,
+                                   const int32_t* block_list, const int32_t* block_count, int32_t list_cap,
+                                   float softmax_scale, uint16_t* dq, uint16_t* dk, uint16_t* dv, void* workspace,
+                                   int64_t workspace_bytes, void* stream)
+{
+    Derived d;
+    lf_status st = check_shape(shape, &d);
+    if (st != LF_OK) return st;
+    if (list_cap < 0) return LF_ERR_CAP;
+    if (!std::isfinite(softmax_scale)) return LF_ERR_ARG;
+    if (!q || !k || !v || !out || !dout || !lse || !block_list || !block_count || !dq || !dk || !dv || !workspace)
+        return LF_ERR_NULL;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) ||
+        !aligned16(out_lo) || !aligned16(dout) || !aligned16(lse) ||
+        !aligned16(block_list) || !aligned16(block_count) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv) ||
+        !aligned16(workspace))
+        return LF_ERR_ALIGN;
+    const BwdPlan plan = bwd_plan(d);
+    if (workspace_bytes < plan.bytes) return LF_ERR_SCRATCH;
+    if ((st = check_device()) != LF_OK) return st;
+    int* err = nullptr;
+    if ((st = error_word(&err)) != LF_OK) return st;
+    const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(static_cast<float>(d.D));
+    lf::AttnBwdMaps m;
+    if (!encode_frames(&m.q, q, d, d.n_cur, d.Lq) || !encode_frames(&m.dout, dout, d, d.n_cur, d.Lq) ||
+        !encode_frames(&m.k, k, d, d.NF, d.kv_stride) || !encode_frames(&m.v, v, d, d.NF, d.kv_stride))
+        return LF_ERR_CUDA;
+    char* ws = static_cast<char*>(workspace);
+    lf::AttnBwdArgs a = {};
+    a.out = out;
+    a.out_lo = out_lo;
+    a.dout = dout;
+    a.lse = lse;
+    a.block_list = block_list;
+    a.block_count = block_count;
+    a.delta = reinterpret_cast<float*>(ws + plan.delta);
+    a.row_list = reinterpret_cast<int*>(ws + plan.row_list);
+    a.row_count = reinterpret_cast<int*>(ws + plan.row_count);
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.BH = d.B * d.H;
+    a.list_cap = list_cap;
+    a.Rq = d.Rq;
+    a.Nkv = d.Nkv;
+    a.bpf = d.bpf;
+    a.F = d.F;
+    a.rem = d.rem;
+    a.n_cur = d.n_cur;
+    a.NF = d.NF;
+    a.Lq = d.Lq;
+    a.kv_stride = d.kv_stride;
+    a.scale = scale;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.err = err;
+    return launch_status(lf::launch_attn_bwd(m, a, d.D, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+lf_status attn_bf16(const lf_hsa_shape* shape, const uint16_t* q, const uint16_t* k, const uint16_t* v,
+                    const int32_t* block_list, const int32_t* block_count, int32_t list_cap, float softmax_scale,
+                    uint16_t* out, uint16_t* out_lo, float* lse, int32_t tail_pieces, void* workspace,
+                    int64_t workspace_bytes, void* stream)
+{
     Derived d;
     lf_status st = check_shape(shape, &d);
     if (st != LF_OK) return st;
@@ -435,12 +584,7 @@ lf_status lf_block_sparse_attn_ws(const lf_hsa_shape* shape, const uint16_t* q, 
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(block_list) || !aligned16(block_count) ||
         !aligned16(out) || (workspace_bytes > 0 && !aligned16(workspace)))
         return LF_ERR_ALIGN;
-    int dev = 0, major = 0, minor = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return LF_ERR_NO_DEVICE;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-        return LF_ERR_NO_DEVICE;
-    if (major != 10 || minor != 0) return LF_ERR_NO_DEVICE;
+    if ((st = check_device()) != LF_OK) return st;
     int* err = nullptr;
     if ((st = error_word(&err)) != LF_OK) return st;
     const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(static_cast<float>(d.D));
@@ -461,15 +605,23 @@ lf_status lf_block_sparse_attn_ws(const lf_hsa_shape* shape, const uint16_t* q, 
     if (workspace_bytes > 0 && tail_pieces != 1) {
         int sm = 0;
         if ((st = sm_count(&sm)) != LF_OK) return st;
-        split_plan(n_rows, sm, list_cap, tail_pieces, workspace_bytes / split_slot_bytes(d.D), &tail, &pieces);
+        split_plan(n_rows, sm, list_cap, tail_pieces, workspace_bytes / (split_slot_bytes(d.D) + (out_lo ? 64 * 4 : 0)),
+                   &tail, &pieces);
     }
     float* part_o = static_cast<float*>(workspace);
     float* part_ml = pieces ? part_o + static_cast<long long>(tail) * pieces * 64 * d.D : nullptr;
     lf::AttnArgs a{block_list, block_count, out, list_cap, d.Rq, d.bpf, d.F, d.Lq, d.Nkv, d.rem, d.kv_stride,
                    scale * 1.4426950408889634f, err, static_cast<int>(n_rows - tail), pieces, part_o, part_ml,
                    static_cast<int>(n_rows), static_cast<int>(n_rows - tail + static_cast<long long>(tail) * pieces)};
+    a.part_lt = pieces ? part_ml + static_cast<long long>(tail) * pieces * 64 * 2 : nullptr;
+    a.lse = lse;
+    a.out_lo = out_lo;
     return launch_status(lf::launch_attn(m, a, d.D, interleaved, static_cast<cudaStream_t>(stream)));
 }
+
+}  // namespace
+
+extern "C" {
 
 lf_status lf_block_sparse_attn_fp8(const lf_hsa_shape* shape, const uint8_t* q8, const uint8_t* k8,
                                    const float* q_scale, const float* k_scale, const uint16_t* v,
@@ -490,12 +642,7 @@ lf_status lf_block_sparse_attn_fp8(const lf_hsa_shape* shape, const uint8_t* q8,
         !aligned16(block_list) || !aligned16(block_count) || !aligned16(out) ||
         (workspace_bytes > 0 && !aligned16(workspace)))
         return LF_ERR_ALIGN;
-    int dev = 0, major = 0, minor = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return LF_ERR_NO_DEVICE;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-        return LF_ERR_NO_DEVICE;
-    if (major != 10 || minor != 0) return LF_ERR_NO_DEVICE;
+    if ((st = check_device()) != LF_OK) return st;
     int* err = nullptr;
     if ((st = error_word(&err)) != LF_OK) return st;
     const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(static_cast<float>(d.D));
@@ -523,6 +670,245 @@ lf_status lf_block_sparse_attn_fp8(const lf_hsa_shape* shape, const uint8_t* q8,
                    static_cast<int>(n_rows), static_cast<int>(n_rows - tail + static_cast<long long>(tail) * pieces),
                    q_scale, k_scale};
     return launch_status(lf::launch_attn_fp8(m, a, v_il, static_cast<cudaStream_t>(stream)));
+}
+
+lf_status lf_rope_plan_init(lf_rope_plan* plan, int32_t head_dim, int32_t rot_dim, int32_t layout, int32_t n_axes,
+                            const int32_t* axis_dims, double base, int32_t scaling, double factor, double original,
+                            double beta_fast, double beta_slow)
+{
+    if (!plan) return LF_ERR_NULL;
+    if (head_dim < 2 || head_dim > 2 * lf::ROPE_MAX_PAIRS || rot_dim < 2 || rot_dim > head_dim || rot_dim % 2 != 0)
+        return LF_ERR_SHAPE;
+    if (n_axes < 1 || n_axes > 3 || (!axis_dims && n_axes != 1)) return LF_ERR_SHAPE;
+    if (layout != LF_ROPE_INTERLEAVED && layout != LF_ROPE_HALF) return LF_ERR_ARG;
+    if (scaling < LF_ROPE_NONE || scaling > LF_ROPE_YARN) return LF_ERR_ARG;
+    if (!(base > 1.0) || !std::isfinite(base)) return LF_ERR_ARG;
+    if (scaling != LF_ROPE_NONE && (!(factor >= 1.0) || !std::isfinite(factor))) return LF_ERR_ARG;
+    int dims[3] = {rot_dim, 0, 0};
+    long long sum = 0;
+    for (int a = 0; a < n_axes; ++a) {
+        if (axis_dims) dims[a] = axis_dims[a];
+        if (dims[a] < 2 || dims[a] % 2 != 0) return LF_ERR_SHAPE;
+        sum += dims[a];
+    }
+    if (sum != rot_dim) return LF_ERR_SHAPE;
+    const double two_pi = 6.283185307179586476925286766559;
+    const double d0 = dims[0];
+    double lo = 0.0, hi = 0.0;
+    if (scaling == LF_ROPE_NTK && dims[0] <= 2) return LF_ERR_SHAPE;
+    if (scaling == LF_ROPE_YARN) {
+        if (!(original > 0.0) || !std::isfinite(original) || !(beta_slow > 0.0) || !(beta_fast > beta_slow) ||
+            !std::isfinite(beta_fast))
+            return LF_ERR_ARG;
+        const double per = d0 / (2.0 * std::log(base));
+        lo = std::min(std::max(std::floor(per * std::log(original / (two_pi * beta_fast))), 0.0), d0 - 1.0);
+        hi = std::min(std::max(std::ceil(per * std::log(original / (two_pi * beta_slow))), 0.0), d0 - 1.0);
+    }
+    std::memset(plan, 0, sizeof *plan);
+    plan->head_dim = head_dim;
+    plan->rot_dim = rot_dim;
+    plan->layout = layout;
+    plan->n_axes = n_axes;
+    plan->amplitude = scaling == LF_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.0f;
+    int pair = 0;
+    for (int a = 0; a < n_axes; ++a) {
+        plan->axis_dims[a] = dims[a];
+        for (int j = 0; j < dims[a] / 2; ++j, ++pair) {
+            double b = base;
+            if (a == 0 && scaling == LF_ROPE_NTK) b *= std::pow(factor, d0 / (d0 - 2.0));
+            double f = std::pow(b, -2.0 * j / dims[a]);
+            if (a == 0 && scaling == LF_ROPE_LINEAR) f /= factor;
+            if (a == 0 && scaling == LF_ROPE_YARN) {
+                const double r = std::min(std::max((j - lo) / std::max(hi - lo, 0.001), 0.0), 1.0);
+                f = f * (1.0 - r) + f / factor * r;
+            }
+            plan->turns[pair] = f / two_pi;
+        }
+    }
+    return LF_OK;
+}
+
+lf_status lf_rope(const lf_rope_plan* plan, int32_t batch, int32_t tokens, int32_t dtype, const int32_t* positions,
+                  int64_t pos_batch_stride, const lf_rope_io* io, int32_t n_io, int32_t backward, void* stream)
+{
+    if (!plan || !io) return LF_ERR_NULL;
+    if (n_io < 1 || n_io > lf::ROPE_MAX_IO || batch < 0 || tokens < 0) return LF_ERR_SHAPE;
+    if (dtype != LF_F32 && dtype != LF_BF16 && dtype != LF_F16) return LF_ERR_ARG;
+    const int D = plan->head_dim, rot = plan->rot_dim;
+    if (D < 2 || D > 2 * lf::ROPE_MAX_PAIRS || rot < 2 || rot > D || rot % 2 != 0 || plan->n_axes < 1 ||
+        plan->n_axes > 3 || (plan->layout != LF_ROPE_INTERLEAVED && plan->layout != LF_ROPE_HALF))
+        return LF_ERR_ARG;
+    long long sum = 0;
+    for (int a = 0; a < plan->n_axes; ++a) {
+        if (plan->axis_dims[a] < 2 || plan->axis_dims[a] % 2 != 0) return LF_ERR_ARG;
+        sum += plan->axis_dims[a];
+    }
+    if (sum != rot || pos_batch_stride < 0) return LF_ERR_ARG;
+    for (int k = 0; k < n_io; ++k)
+        if (io[k].heads < 1 || io[k].heads > 16384) return LF_ERR_SHAPE;
+    if (batch == 0 || tokens == 0) return LF_OK;
+    if (static_cast<long long>(batch) * tokens * D >= (1ll << 31)) return LF_ERR_SHAPE;
+    if (!positions) return LF_ERR_NULL;
+    const int size = dtype == LF_F32 ? 4 : 2, elems = 16 / size;
+    if ((reinterpret_cast<uintptr_t>(positions) & 3u) != 0) return LF_ERR_ALIGN;
+    lf::RopeArgs a = {};
+    const bool half = plan->layout == LF_ROPE_HALF;
+    bool vec = (half ? rot / 2 : rot) % elems == 0 && (D - rot) % elems == 0;
+    for (int k = 0; k < n_io; ++k) {
+        if (!io[k].x || !io[k].out) return LF_ERR_NULL;
+        const uintptr_t both = reinterpret_cast<uintptr_t>(io[k].x) | reinterpret_cast<uintptr_t>(io[k].out);
+        if (both % size != 0) return LF_ERR_ALIGN;
+        vec = vec && both % 16 == 0;
+        const int extent[3] = {batch, io[k].heads, tokens};
+        a.io[k].x = io[k].x;
+        a.io[k].out = io[k].out;
+        a.io[k].heads = io[k].heads;
+        a.io[k].rotate = io[k].rotate != 0;
+        for (int i = 0; i < 3; ++i) {
+            const int64_t xs = io[k].x_stride[i], os = io[k].out_stride[i];
+            if (xs < 0 || os < 0 || (os == 0 && extent[i] > 1)) return LF_ERR_ARG;
+            a.io[k].xs[i] = extent[i] > 1 ? xs : 0;
+            a.io[k].os[i] = extent[i] > 1 ? os : 0;
+            vec = vec && a.io[k].xs[i] % elems == 0 && a.io[k].os[i] % elems == 0;
+        }
+    }
+    a.n_io = n_io;
+    a.batch = batch;
+    a.tokens = tokens;
+    a.head_dim = D;
+    a.rot_dim = rot;
+    a.n_axes = plan->n_axes;
+    a.axis_end[0] = plan->axis_dims[0] / 2;
+    a.axis_end[1] = a.axis_end[0] + (plan->n_axes > 1 ? plan->axis_dims[1] / 2 : 0);
+    if (plan->n_axes < 2) a.axis_end[0] = lf::ROPE_MAX_PAIRS;
+    if (plan->n_axes < 3) a.axis_end[1] = lf::ROPE_MAX_PAIRS;
+    a.amplitude = plan->amplitude;
+    a.backward = backward != 0;
+    a.positions = positions;
+    a.pos_batch = pos_batch_stride;
+    for (int p = 0; p < rot / 2; ++p) {
+        if (!std::isfinite(plan->turns[p])) return LF_ERR_ARG;
+        a.turns[p] = plan->turns[p];
+    }
+    return launch_status(lf::launch_rope(a, dtype, half, vec, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+lf_status check_norm(const lf_norm_gate_shape* s, const lf_norm_gate_vectors* v, bool has_y, bool has_h)
+{
+    if (!s) return LF_ERR_NULL;
+    if (s->rows < 0 || s->rows >= (1ll << 31) || s->rows_per_group < 1 || s->dim < 1 || s->dim > lf::NORM_MAX_DIM)
+        return LF_ERR_SHAPE;
+    const bool known = s->x_dtype >= LF_F32 && s->x_dtype <= LF_F16 && s->y_dtype >= LF_F32 && s->y_dtype <= LF_F16;
+    if (!known || (s->x_dtype != s->y_dtype && s->x_dtype != LF_F32)) return LF_ERR_ARG;
+    if (s->pre_norm < LF_NORM_NONE || s->pre_norm > LF_NORM_LAYER || s->post_norm < LF_NORM_NONE ||
+        s->post_norm > LF_NORM_LAYER)
+        return LF_ERR_ARG;
+    if (!(s->eps >= 0.f) || !std::isfinite(s->eps) || !std::isfinite(s->residual_scale)) return LF_ERR_ARG;
+    if (has_h && s->pre_norm == LF_NORM_NONE) return LF_ERR_ARG;
+    if (!has_y && s->post_norm != LF_NORM_NONE) return LF_ERR_ARG;
+    if (v) {
+        if ((v->post_w || v->post_b) && s->post_norm == LF_NORM_NONE) return LF_ERR_ARG;
+        if ((v->scale || v->shift || v->pre_w || v->pre_b) && s->pre_norm == LF_NORM_NONE) return LF_ERR_ARG;
+        if (v->gate && !has_y) return LF_ERR_ARG;
+        const float* p[7] = {v->gate, v->scale, v->shift, v->pre_w, v->pre_b, v->post_w, v->post_b};
+        for (const float* q : p)
+            if (q && !aligned16(q)) return LF_ERR_ALIGN;
+    }
+    return LF_OK;
+}
+
+// Rows of a group, at most the call's rows (so that products with it stay small).
+long long norm_group_rows(const lf_norm_gate_shape* s)
+{
+    return std::min<long long>(s->rows_per_group, std::max<long long>(s->rows, 1));
+}
+
+lf::NormArgs norm_args(const lf_norm_gate_shape* s, const lf_norm_gate_vectors* v)
+{
+    lf::NormArgs a = {};
+    if (v) a.v = {v->gate, v->scale, v->shift, v->pre_w, v->pre_b, v->post_w, v->post_b};
+    a.rows = s->rows;
+    a.per_group = norm_group_rows(s);
+    a.dim = s->dim;
+    a.pre = s->pre_norm;
+    a.post = s->post_norm;
+    a.eps = s->eps;
+    a.alpha = s->residual_scale;
+    return a;
+}
+
+}  // namespace
+
+lf_status lf_norm_gate(const lf_norm_gate_shape* shape, const lf_norm_gate_vectors* vectors, const void* x,
+                       const void* y, void* r, void* h, void* stream)
+{
+    const bool empty = shape && shape->rows == 0;  // nothing is there, so null pointers say nothing
+    const lf_status st = check_norm(shape, vectors, empty || y, !empty && h);
+    if (st != LF_OK) return st;
+    if (empty) return LF_OK;
+    if (!r && !h) return LF_ERR_NULL;
+    if (!x) return LF_ERR_NULL;
+    if (!aligned16(x) || !aligned16(y) || !aligned16(r) || !aligned16(h)) return LF_ERR_ALIGN;
+    lf::NormArgs a = norm_args(shape, vectors);
+    a.x = x;
+    a.y = y;
+    a.r = r;
+    a.h = h;
+    return launch_status(lf::launch_norm_fwd(a, shape->x_dtype, shape->y_dtype, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t lf_norm_gate_bwd_workspace(const lf_norm_gate_shape* shape)
+{
+    if (check_norm(shape, nullptr, true, false) != LF_OK) return -1;
+    const int64_t per = norm_group_rows(shape), groups = (shape->rows + per - 1) / per;
+    return (lf::norm_bwd_ctas(shape->rows) + groups) * 4 * ((shape->dim + 7) / 8 * 8) * 4;
+}
+
+lf_status lf_norm_gate_bwd(const lf_norm_gate_shape* shape, const lf_norm_gate_vectors* vectors, const void* x,
+                           const void* y, const void* dr, const void* dh, void* dx, void* dy,
+                           const lf_norm_gate_vectors* grads, void* workspace, int64_t workspace_bytes, void* stream)
+{
+    const bool empty = shape && shape->rows == 0;
+    lf_status st = check_norm(shape, vectors, empty || y, !empty && dh);
+    if (st != LF_OK) return st;
+    if ((st = check_norm(shape, grads, empty || y, !empty && dh)) != LF_OK) return st;
+    if (!empty && !y && dy) return LF_ERR_ARG;
+    if (workspace_bytes < 0) return LF_ERR_ARG;
+    if (workspace_bytes < lf_norm_gate_bwd_workspace(shape)) return LF_ERR_SCRATCH;
+    lf::NormArgs a = norm_args(shape, vectors);
+    if (grads) {
+        a.dgate = grads->gate;
+        a.dscale = grads->scale;
+        a.dshift = grads->shift;
+        a.dpre_w = grads->pre_w;
+        a.dpre_b = grads->pre_b;
+        a.dpost_w = grads->post_w;
+        a.dpost_b = grads->post_b;
+    }
+    if (shape->rows == 0) {
+        float* w[4] = {a.dpre_w, a.dpre_b, a.dpost_w, a.dpost_b};
+        for (float* p : w)
+            if (p && cudaMemsetAsync(p, 0, sizeof(float) * shape->dim, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+                return LF_ERR_CUDA;
+        return LF_OK;
+    }
+    if (!x || !workspace) return LF_ERR_NULL;
+    if (!aligned16(x) || !aligned16(y) || !aligned16(dr) || !aligned16(dh) || !aligned16(dx) || !aligned16(dy) ||
+        !aligned16(workspace))
+        return LF_ERR_ALIGN;
+    a.x = x;
+    a.y = y;
+    a.dr = dr;
+    a.dh = dh;
+    a.dx = dx;
+    a.dy = dy;
+    a.part = static_cast<float*>(workspace);
+    a.n_cta = lf::norm_bwd_ctas(shape->rows);
+    a.rows_per_cta = (shape->rows + a.n_cta - 1) / a.n_cta;
+    a.n_cta = static_cast<int>((shape->rows + a.rows_per_cta - 1) / a.rows_per_cta);
+    return launch_status(lf::launch_norm_bwd(a, shape->x_dtype, shape->y_dtype, static_cast<cudaStream_t>(stream)));
 }
 
 lf_status lf_cag_budget(int32_t n_chunks, const double* T, const double* flops_w, double s_base, double s_target,

@@ -133,8 +133,10 @@ struct AttnAux {
     int abort;
     alignas(16) float alpha[2][64];  // per-warpgroup rescale factors of the query columns
     float lsum[2][64];               // softmax denominators of each warpgroup's rows
+    float ltsum[2][64];              // the same sums of the bf16 weights (training)
     alignas(16) float m_s[2][64];    // final running max (log2 units) per warpgroup and query row
     float wgt[2][64];                // epilogue weights of the two accumulators per query row
+    float renorm[64];                // denominator over the sum of the bf16 weights (training)
     int lst[LIST_SMEM];              // the CTA's block list (entries past LIST_SMEM stay in global memory)
 };
 
@@ -468,6 +470,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         uint8_t* prow = smem + L::OFF_P + g * L::P_BYTES + (2 * hh) * L::P_PANEL + qr * 128;
         float m_run = -INFINITY;  // stabiliser of this row (identical in lanes l and l^16)
         float l_run = 0.f;        // this thread's share of the row's softmax denominator
+        float lt_run = 0.f;       // the same of the weights as rounded to bf16 (training)
 
         // e4m3: the key scales of this warpgroup's next step, fetched a step ahead (thread i of
         // the warpgroup holds keys i and i + 128 of the step) so their L2 latency overlaps work
@@ -553,6 +556,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const float m_new = need ? ms : m_run;
             const float alpha = need ? fast_exp2(m_run - m_new) : 1.f;  // 0 when m_run = -inf
             l_run *= alpha;
+            if constexpr (!F8) lt_run *= alpha;
             m_run = m_new;
             // 2. Probabilities (registers), then wait until the PV of this warpgroup's
             // previous step has read its P buffer and finished accumulating into its O^T.
@@ -569,6 +573,12 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 pk[c >> 1] = pack_bf16x2(p0, p1);
             }
             l_run += la + lb;
+            if (!F8 && a.out_lo) {
+                float ta = 0.f, tb = 0.f;
+#pragma unroll
+                for (int c = 0; c < 64; ++c) fadd2_acc(ta, tb, __uint_as_float(pk[c] << 16), __uint_as_float(pk[c] & 0xFFFF0000u));
+                lt_run += ta + tb;
+            }
             if (j > 0) mbar_wait(&x.p_empty[g], (j - 1) & 1, abort_flag, a.err, 0x31);
             // 3. P row -> shared memory (two 64-key panels, 128-byte swizzle).
 #pragma unroll
@@ -614,6 +624,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 
         // ------------------------------------------------------------ epilogue
         const float l_row = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
+        if constexpr (!F8) {
+            const float lt_row = lt_run + __shfl_xor_sync(0xffffffffu, lt_run, 16);
+            if (hh == 0) x.ltsum[g][qr] = lt_row;
+        }
         if (hh == 0) {
             x.lsum[g][qr] = l_row;
             x.m_s[g][qr] = m_run;
@@ -643,10 +657,17 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const float inv = den > 0.f ? 1.f / den : 0.f;
             x.wgt[0][cc] = f0 * inv;
             x.wgt[1][cc] = f1 * inv;
+            // training: the row under the rounded weights, which sum to dent, is the row times den / dent
+            const float dent = F8 ? 0.f : x.ltsum[0][cc] * f0 + x.ltsum[1][cc] * f1;
+            if (!F8 && a.out_lo) x.renorm[cc] = dent > 0.f ? den / dent : 1.f;
             if (slot >= 0) {
                 float* ml = a.part_ml + (static_cast<long long>(slot) * 64 + cc) * 2;
                 ml[0] = den > 0.f ? mx : -INFINITY;
                 ml[1] = den > 0.f ? den : 0.f;
+                if (!F8 && a.out_lo) a.part_lt[static_cast<long long>(slot) * 64 + cc] = den > 0.f ? dent : 0.f;
+            } else if (!F8 && a.lse && cc < q_rows) {
+                // natural log from the base-2 maximum and the fp32 denominator
+                a.lse[q_row0 + cc] = den == 0.f ? -INFINITY : (mx + log2f(den)) * 0.69314718055994531f;
             }
         }
         tmem_ld_wait();
@@ -664,12 +685,16 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 }
             }
         } else {
+            __nv_bfloat16* lstage = ostage + 64 * D;  // the row under the rounded weights, less out (training)
             if (t < D) {
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
                     const int cc = 32 * g + c;
                     const float w0 = x.wgt[0][cc], w1 = x.wgt[1][cc];
-                    ostage[cc * D + t] = __float2bfloat16_rn((w0 != 0.f ? o0[c] * w0 : 0.f) + (w1 != 0.f ? o1[c] * w1 : 0.f));
+                    const float o = (w0 != 0.f ? o0[c] * w0 : 0.f) + (w1 != 0.f ? o1[c] * w1 : 0.f);
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(o);
+                    ostage[cc * D + t] = hi;
+                    if (!F8 && a.out_lo) lstage[cc * D + t] = __float2bfloat16_rn(o * x.renorm[cc] - __bfloat162float(hi));
                 }
             }
             named_bar_sync(3, 256);
@@ -677,8 +702,9 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             for (int idx = tid - W_SOFT0 * 32; idx < chunks; idx += 256) {
                 const int qq = idx / (D / 8);
                 const int c8 = idx - qq * (D / 8);
-                *reinterpret_cast<uint4*>(a.out + (static_cast<long long>(q_row0) + qq) * D + c8 * 8) =
-                    *reinterpret_cast<const uint4*>(ostage + qq * D + c8 * 8);
+                const long long at = (static_cast<long long>(q_row0) + qq) * D + c8 * 8;
+                *reinterpret_cast<uint4*>(a.out + at) = *reinterpret_cast<const uint4*>(ostage + qq * D + c8 * 8);
+                if (!F8 && a.out_lo) *reinterpret_cast<uint4*>(a.out_lo + at) = *reinterpret_cast<const uint4*>(lstage + qq * D + c8 * 8);
             }
         }
     }
@@ -726,12 +752,15 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnArgs a)
     float acc[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] = 0.f;
-    float den = 0.f;
+    float den = 0.f, dent = 0.f;
     for (int p0 = 0; p0 < a.pieces; p0 += 32) {
         float wl = 0.f;
         if (p0 + lane < a.pieces) {
             const float mp = ml[static_cast<long long>(p0 + lane) * 128];
-            if (mp != -INFINITY) wl = fast_exp2(mp - M) * ml[static_cast<long long>(p0 + lane) * 128 + 1];
+            if (mp != -INFINITY) {
+                wl = fast_exp2(mp - M) * ml[static_cast<long long>(p0 + lane) * 128 + 1];
+                if (a.out_lo) dent += fast_exp2(mp - M) * a.part_lt[(s0 + p0 + lane) * 64 + qq];
+            }
         }
         den += wl;
         const int np = min(32, a.pieces - p0);
@@ -753,15 +782,30 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnArgs a)
         }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    for (int o = 16; o > 0; o >>= 1) {
+        den += __shfl_xor_sync(0xffffffffu, den, o);
+        dent += __shfl_xor_sync(0xffffffffu, dent, o);
+    }
+    const float renorm = dent > 0.f ? den / dent : 1.f;  // as in the attention kernel's epilogue
     const float inv = den > 0.f ? 1.f / den : 0.f;
-    uint16_t* out = a.out + q_row * D + V * lane;
+    if (a.lse && lane == 0) a.lse[q_row] = den == 0.f ? -INFINITY : (M + log2f(den)) * 0.69314718055994531f;
+    float rest[V];  // the row under the rounded weights, less out
+    uint32_t hi[V / 2];
+#pragma unroll
+    for (int e = 0; e < V; e += 2) {
+        acc[e] *= inv;
+        acc[e + 1] *= inv;
+        hi[e / 2] = pack_bf16x2(acc[e], acc[e + 1]);
+        rest[e] = acc[e] * renorm - __uint_as_float(hi[e / 2] << 16);
+        rest[e + 1] = acc[e + 1] * renorm - __uint_as_float(hi[e / 2] & 0xFFFF0000u);
+    }
+    const long long at = q_row * D + V * lane;
     if constexpr (V == 4) {
-        const uint32_t lo = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-        const uint32_t hi = pack_bf16x2(acc[2] * inv, acc[3] * inv);
-        *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
+        *reinterpret_cast<uint2*>(a.out + at) = make_uint2(hi[0], hi[1]);
+        if (a.out_lo) *reinterpret_cast<uint2*>(a.out_lo + at) = make_uint2(pack_bf16x2(rest[0], rest[1]), pack_bf16x2(rest[2], rest[3]));
     } else {
-        *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+        *reinterpret_cast<uint32_t*>(a.out + at) = hi[0];
+        if (a.out_lo) *reinterpret_cast<uint32_t*>(a.out_lo + at) = pack_bf16x2(rest[0], rest[1]);
     }
 }
 

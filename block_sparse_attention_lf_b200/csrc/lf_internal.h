@@ -95,6 +95,10 @@ struct AttnArgs {
     int n_units;          // CTAs of the attention grid: n_whole whole lists + (n_rows - n_whole) * pieces pieces
     const float* q_scale;  // e4m3 path: per-token scales of q8 [B*H*Lq] and k8 [B*H*kv_stride]
     const float* k_scale;
+    float* lse;  // [B*H*Lq] natural log-sum-exp of each row; null: not wanted
+    uint16_t* out_lo;  // like out: the row under the bf16 weights (normalised by their own sum), less out;
+                       // null: not wanted
+    float* part_lt;    // [slot][64]: a piece's sum of the bf16 weights, where out_lo is wanted
 };
 
 struct AttnMaps {

@@ -29,6 +29,18 @@
  *                        allocate: its scratch is an array inside the library
  *   lf_quant_fp8_rows    per-token e4m3 codes and scales (the FP8 attention's q, k)
  *   lf_block_sparse_attn_fp8  the attention with e4m3 q and k (tcgen05 kind::f8f6f4)
+ *   lf_block_sparse_attn_lse  the attention with each row's log-sum-exp (training)
+ *   lf_block_sparse_attn_bwd  its gradient in q, k and v over the same lists
+ *   lf_attn_bwd_workspace     the gradient's workspace size (host only)
+ *
+ * and what stands on both sides of the call in a transformer block:
+ *
+ *   lf_rope              rotary positions of q and k (and the move of v) from a
+ *                        projection's layout to the call's, and the gradient
+ *   lf_rope_plan_init    its frequencies (host only)
+ *   lf_norm_gate         norm after a block, gate, residual sum, norm before the
+ *                        next block and its modulation in one pass
+ *   lf_norm_gate_bwd     its gradients; lf_norm_gate_bwd_workspace sizes the workspace
  *
  * plus the host-side Chunk-Aware Growth budget solver (same pages, stage 1 /
  * Technical Summary 2.1).
@@ -89,7 +101,8 @@ typedef enum lf_status {
     LF_ERR_ARG = 9,            /* another invalid scalar (chunk index, sparsity, scale) */
     LF_ERR_LIST = 10,          /* device error word: a block id or count out of range */
     LF_ERR_NO_DEVICE = 11,     /* no usable sm_100 device */
-    LF_ERR_SCRATCH = 12        /* the call needs more than the library's static scratch array */
+    LF_ERR_SCRATCH = 12        /* the call needs more than the library's static scratch array, or than the
+                                  workspace that it was given */
 } lf_status;
 
 /*
@@ -413,6 +426,203 @@ LF_API lf_status lf_block_sparse_attn_fp8(const lf_hsa_shape* shape, const uint8
                                    const int32_t* block_list, const int32_t* block_count, int32_t list_cap,
                                    float softmax_scale, uint16_t* out, int32_t tail_pieces,
                                    void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Fine-tuning under sparsity (163.com article, section 4: the ablation recovers
+ * its quality by fine-tuning) needs the attention's gradient. Forward: the same
+ * attention and arguments as lf_block_sparse_attn_ws, which also writes
+ *   out_lo  [B,H,Lq,D] bf16, for the gradient; NULL: not wanted. out + out_lo is, to
+ *        2^-16, the row under the softmax weights as the tensor cores use them (rounded
+ *        to bf16) and normalised by their own sum, where out divides by the fp32 sum.
+ *        With it a piece slot of the workspace takes 64 * (head_dim + 3) * 4 bytes.
+ *   lse  [B,H,Lq] fp32: log sum_s exp(scale * <q_t, k_s>) over the row's listed
+ *        tokens (natural log); -inf for a row whose list is empty.
+ * out is bit-identical to lf_block_sparse_attn_ws. Two partial results over
+ * disjoint lists combine through their lse.
+ * Errors: those of lf_block_sparse_attn_ws; LF_ERR_NULL / LF_ERR_ALIGN for lse.
+ */
+LF_API lf_status lf_block_sparse_attn_lse(const lf_hsa_shape* shape, const uint16_t* q, const uint16_t* k,
+                                   const uint16_t* v, const int32_t* block_list, const int32_t* block_count,
+                                   int32_t list_cap, float softmax_scale, uint16_t* out, uint16_t* out_lo,
+                                   float* lse, int32_t tail_pieces, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of lf_block_sparse_attn_bwd for a shape (host only); -1 on a bad shape. */
+LF_API int64_t lf_attn_bwd_workspace(const lf_hsa_shape* shape);
+
+/*
+ * Gradient of lf_block_sparse_attn in q, k and v; the lists are constants (the
+ * selection has no gradient). With s = scale, P = exp(s q k^T - lse) over the
+ * listed tokens and delta_t = <dout_t, out_t>:
+ *   dS = P * (dout v^T - delta),  dq = s dS k,  dk = s dS^T q,  dv = P^T dout.
+ *   out, out_lo, lse  as written by lf_block_sparse_attn_lse for the same arguments
+ *                (softmax_scale among them). out_lo may be NULL; delta then carries the
+ *                roundings of out and of the forward's weights, which show where a row
+ *                attends to few keys or sharply.
+ *   dout         [B,H,Lq,D] bf16: gradient of out
+ *   dq           [B,H,Lq,D] bf16: every valid query row is written (zeros where
+ *                the list is empty)
+ *   dk, dv       [B,H,kv_stride,D] bf16: the n_frames*frame_tokens tokens of every
+ *                head are written (zeros where no list names them); rows between
+ *                them and kv_stride are left as they are
+ *   workspace    lf_attn_bwd_workspace(shape) bytes, 16-byte aligned, owned by the
+ *                caller; its contents need not be kept between calls. Two calls in
+ *                flight at once (or two captured graphs replayed at once) need two.
+ * Products run on the tensor cores in bf16 with fp32 accumulation (P and dS are
+ * rounded to bf16 once); sums are taken in a fixed order, so the same arguments
+ * give the same bits. A list must name no block twice: a repeated block is reported
+ * as LF_ERR_LIST by lf_get_device_error(), and that call's gradients are then
+ * unspecified. Ids and counts out of range are treated and reported as in
+ * lf_block_sparse_attn. Outputs must not overlap inputs.
+ * Errors: LF_ERR_NULL, LF_ERR_ALIGN, LF_ERR_SHAPE, LF_ERR_CAP, LF_ERR_ARG
+ * (softmax_scale not finite), LF_ERR_SCRATCH (workspace_bytes too small),
+ * LF_ERR_NO_DEVICE, LF_ERR_CUDA.
+ */
+LF_API lf_status lf_block_sparse_attn_bwd(const lf_hsa_shape* shape, const uint16_t* q, const uint16_t* k,
+                                   const uint16_t* v, const uint16_t* out, const uint16_t* out_lo,
+                                   const uint16_t* dout, const float* lse,
+                                   const int32_t* block_list, const int32_t* block_count, int32_t list_cap,
+                                   float softmax_scale, uint16_t* dq, uint16_t* dk, uint16_t* dv, void* workspace,
+                                   int64_t workspace_bytes, void* stream);
+
+/* Element types of the block-level operators below. */
+typedef enum lf_dtype { LF_F32 = 0, LF_BF16 = 1, LF_F16 = 2 } lf_dtype;
+
+/*
+ * Rotary positions. The pages' deployment stack fuses them with the attention's
+ * inputs (gist.science, Technical Summary 4: fused rotary and norm kernels); the
+ * formulas are the standard ones.
+ * Pairs i = 0 .. rot_dim/2 - 1 of a head's first rot_dim elements turn; the other
+ * elements are copied. Interleaved layout: pair i is (2i, 2i+1); half layout:
+ * (i, i + rot_dim/2). Up to three axes (text: one; video: time, height, width) own
+ * consecutive pairs: axis a has axis_dims[a]/2 of them, with frequency
+ *   f_j = base^(-2j / axis_dims[a]),  j counting within the axis.
+ * Scaling for contexts longer than trained acts on axis 0:
+ *   LF_ROPE_LINEAR  f_j / factor
+ *   LF_ROPE_NTK     base replaced by base * factor^(d / (d - 2)), d = axis_dims[0] > 2
+ *   LF_ROPE_YARN    f_j (1 - r_j) + r_j f_j / factor, r_j = clamp((j - lo) / (hi - lo)),
+ *                   lo, hi = floor, ceil of d ln(original / (2 pi beta)) / (2 ln base) at
+ *                   beta = beta_fast, beta_slow, within [0, d - 1]; every rotated element
+ *                   times 0.1 ln(factor) + 1
+ */
+typedef enum lf_rope_layout { LF_ROPE_INTERLEAVED = 0, LF_ROPE_HALF = 1 } lf_rope_layout;
+typedef enum lf_rope_scaling { LF_ROPE_NONE = 0, LF_ROPE_LINEAR = 1, LF_ROPE_NTK = 2, LF_ROPE_YARN = 3 } lf_rope_scaling;
+
+/* Frequencies of a head, filled by lf_rope_plan_init and kept by the caller. */
+typedef struct lf_rope_plan {
+    int32_t head_dim;      /* 2 .. 256 */
+    int32_t rot_dim;       /* even, 2 .. head_dim */
+    int32_t layout;        /* lf_rope_layout */
+    int32_t n_axes;        /* 1 .. 3 */
+    int32_t axis_dims[3];  /* even, sum rot_dim */
+    float amplitude;       /* factor on the rotated elements (1 but for LF_ROPE_YARN) */
+    double turns[128];     /* revolutions per position of each pair: f / (2 pi) */
+} lf_rope_plan;
+
+/*
+ * Fills a plan (host only, fp64). axis_dims NULL: one axis of rot_dim.
+ * base > 1; factor >= 1 (ignored by LF_ROPE_NONE); original, beta_fast >
+ * beta_slow > 0 only for LF_ROPE_YARN.
+ * Errors: LF_ERR_NULL, LF_ERR_SHAPE (dims), LF_ERR_ARG (the other values).
+ */
+LF_API lf_status lf_rope_plan_init(lf_rope_plan* plan, int32_t head_dim, int32_t rot_dim, int32_t layout, int32_t n_axes,
+                            const int32_t* axis_dims, double base, int32_t scaling, double factor, double original,
+                            double beta_fast, double beta_slow);
+
+/*
+ * One tensor of an lf_rope call: element (b, h, t, e) is at b*stride[0] + h*stride[1]
+ * + t*stride[2] + e, strides in elements and >= 0, so a slice of a fused token-major
+ * projection and a slot of a head-major cache are both given as they are. An output
+ * stride must not be 0 where its extent is above 1. out == x with equal strides
+ * rotates in place; otherwise the two must not overlap.
+ */
+typedef struct lf_rope_io {
+    const void* x;
+    void* out;
+    int64_t x_stride[3];
+    int64_t out_stride[3];
+    int32_t heads;         /* >= 1; may differ between the call's tensors */
+    int32_t rotate;        /* 0: the tensor is copied (a value projection) */
+} lf_rope_io;
+
+/*
+ * Rotates n_io (1 .. 3) tensors of batch x heads x tokens x head_dim elements of
+ * `dtype` in one launch.
+ *   positions     [batch][tokens][n_axes] int32, any sign; pos_batch_stride elements
+ *                 between samples, 0 when they share one [tokens][n_axes] table.
+ *                 Angles are formed in fp64, so far positions keep fp32 accuracy.
+ *   backward      != 0: the gradient, x being the gradient of the forward's output
+ *                 (angles negated; the same amplitude).
+ * Pointers need the element's alignment; 16-byte aligned pointers and strides take
+ * the wide path. tokens == 0 or batch == 0 does nothing.
+ * Errors: LF_ERR_NULL, LF_ERR_ALIGN, LF_ERR_SHAPE (sizes; 2^31 or more token units),
+ * LF_ERR_ARG (dtype, strides, plan contents), LF_ERR_CUDA.
+ */
+LF_API lf_status lf_rope(const lf_rope_plan* plan, int32_t batch, int32_t tokens, int32_t dtype,
+                  const int32_t* positions, int64_t pos_batch_stride, const lf_rope_io* io, int32_t n_io,
+                  int32_t backward, void* stream);
+
+/*
+ * The step between two blocks of a diffusion transformer (gist.science, Technical
+ * Summary 4: fused norm kernels), one pass over [rows, dim]:
+ *   u = post(y) * post_w + post_b
+ *   r = residual_scale * x + gate * u              the residual stream
+ *   h = (pre(r) * pre_w + pre_b) * (1 + scale) + shift   the next block's input
+ * post and pre: none, RMS norm t / sqrt(mean t^2 + eps) or layer norm
+ * (t - mean) / sqrt(var + eps) over the row. gate, scale and shift belong to groups
+ * of rows_per_group consecutive rows (a frame's tokens, a sample); the last group
+ * may be shorter.
+ *   rows >= 0, 1 <= dim <= 16384, rows_per_group >= 1
+ *   x_dtype of x, r, dr, dx; y_dtype of y, h, dh, dy: equal, or x fp32 with y 16-bit
+ *   eps >= 0, residual_scale finite
+ * h is formed from the fp32 r, not from the stored one.
+ */
+typedef enum lf_norm_kind { LF_NORM_NONE = 0, LF_NORM_RMS = 1, LF_NORM_LAYER = 2 } lf_norm_kind;
+
+typedef struct lf_norm_gate_shape {
+    int64_t rows;
+    int64_t rows_per_group;
+    int32_t dim;
+    int32_t x_dtype, y_dtype;
+    int32_t pre_norm, post_norm;  /* lf_norm_kind */
+    float eps;
+    float residual_scale;
+} lf_norm_gate_shape;
+
+/* Vectors of the step, fp32, NULL where absent (gate, weights 1; the others 0):
+ * gate, scale, shift [groups, dim]; the weights and biases [dim]. post_* need a post
+ * norm, the others but gate a pre norm. In lf_norm_gate_bwd the same struct of
+ * outputs: a gradient is written where its pointer is not NULL. */
+typedef struct lf_norm_gate_vectors {
+    float *gate, *scale, *shift, *pre_w, *pre_b, *post_w, *post_b;
+} lf_norm_gate_vectors;
+
+/*
+ *   y  NULL: no block output (r = residual_scale * x); post none and no gate then
+ *   r  NULL: not stored;  h NULL: no next norm (needed when pre is none)
+ * r may be x and h may be y (same pointer); other overlaps are not allowed.
+ * All pointers 16-byte aligned, rows contiguous. vectors may be NULL (all absent).
+ * Errors: LF_ERR_NULL, LF_ERR_ALIGN, LF_ERR_SHAPE, LF_ERR_ARG, LF_ERR_CUDA.
+ */
+LF_API lf_status lf_norm_gate(const lf_norm_gate_shape* shape, const lf_norm_gate_vectors* vectors, const void* x,
+                       const void* y, void* r, void* h, void* stream);
+
+/* Workspace bytes of lf_norm_gate_bwd (host only); -1 on a bad shape. */
+LF_API int64_t lf_norm_gate_bwd_workspace(const lf_norm_gate_shape* shape);
+
+/*
+ * Gradients of lf_norm_gate from the forward's own inputs (nothing has to be saved:
+ * r and the statistics are formed again in fp32).
+ *   dr  gradient of r from its other uses, NULL: none;  dh gradient of h, NULL: none
+ *   dx, dy  NULL: not wanted. grads: see lf_norm_gate_vectors; may be NULL.
+ *   workspace  lf_norm_gate_bwd_workspace(shape) bytes, 16-byte aligned; two calls in
+ *   flight at once need two.
+ * dx may be dr or x, and dy may be dh or y (same pointer). Column sums are added in a
+ * fixed order. rows == 0 writes zeros to the weights' gradients (there are no groups).
+ * Errors: those of lf_norm_gate; LF_ERR_SCRATCH (workspace_bytes too small).
+ */
+LF_API lf_status lf_norm_gate_bwd(const lf_norm_gate_shape* shape, const lf_norm_gate_vectors* vectors, const void* x,
+                           const void* y, const void* dr, const void* dh, void* dx, void* dy,
+                           const lf_norm_gate_vectors* grads, void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
  * Chunk-Aware Growth budget solver, host only, fp64 (paper.rainbus.top,
