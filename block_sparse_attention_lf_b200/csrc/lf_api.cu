@@ -230,10 +230,10 @@ bool encode_frames(CUtensorMap* m, const void* base, const Derived& d, int frame
     return r == CUDA_SUCCESS;
 }
 
-// Workspace of the attention's gradient: each row's delta, and for each KV block the query
+// Workspace of the attention's gradient: the work counters, each row's delta, and for each KV block the query
 // blocks that list it (ascending) with their number.
 struct BwdPlan {
-    long long delta, row_count, row_list, bytes;
+    long long next_item, delta, row_count, row_list, bytes;
 };
 
 BwdPlan bwd_plan(const Derived& d)
@@ -241,8 +241,9 @@ BwdPlan bwd_plan(const Derived& d)
     const long long BH = static_cast<long long>(d.B) * d.H;
     auto up = [](long long n) { return (n + 255) / 256 * 256; };
     BwdPlan p;
-    p.delta = 0;
-    p.row_count = up(BH * d.Lq * 4);
+    p.next_item = 0;
+    p.delta = 256;
+    p.row_count = p.delta + up(BH * d.Lq * 4);
     p.row_list = p.row_count + up(BH * d.Nkv * 4);
     p.bytes = p.row_list + up(BH * d.Nkv * d.Rq * 4);
     return p;
@@ -542,6 +543,7 @@ lf_status lf_block_sparse_attn_bwd(const lf_hsa_shape* shape, const uint16_t* q,
     a.block_list = block_list;
     a.block_count = block_count;
     a.delta = reinterpret_cast<float*>(ws + plan.delta);
+    a.next_item = reinterpret_cast<int*>(ws + plan.next_item);
     a.row_list = reinterpret_cast<int*>(ws + plan.row_list);
     a.row_count = reinterpret_cast<int*>(ws + plan.row_count);
     a.dq = dq;

@@ -10,22 +10,22 @@
 // of dout v^T under weights that sum to one exactly: their roundings then weigh only the
 // differences (dout v^T - delta), as dS's own rounding does.
 //
-// Two kernels of one shape, so that every sum has a fixed order and no value is added
-// atomically: the query side (a CTA per query block, its KV block list streamed) forms dq,
-// the key side (a CTA per KV block, the query blocks that list it streamed) forms dk and
-// dv. Both form P and dS anew: 7 products instead of 5, for no fp32 dq in memory and the
-// same bits on every run. The key side's lists are the transposed block lists, built by a
-// small kernel before.
+// Every sum has a fixed order and no value is added atomically. A query item (one query block,
+// its KV block list streamed) forms dq, a key item (one KV block, the query blocks that list it
+// streamed) forms dk and dv. Both form P and dS anew: 7 products instead of 5, for no fp32 dq in
+// memory and the same bits on every run. The key items' lists are the transposed block lists,
+// which a preparing kernel builds beside delta.
 //
-// One CTA holds the 64 rows of its own block (X0, Y0) in shared memory and streams tiles of
-// two listed blocks (Xs, Ys, 128 rows):
-//                 X0   Y0     Xs   Ys
-//   query side    q    dout   k    v
-//   key side      k    v      q    dout
+// An item keeps the 64 rows of its own block (X0, Y0) in shared memory and streams tiles of two
+// listed blocks (Xs, Ys, 128 rows):
+//                X0   Y0     Xs   Ys
+//   query item   q    dout   k    v
+//   key item     k    v      q    dout
 //   S' = Xs X0^T and dP' = Ys Y0^T (M = 128 streamed rows, N = 64, K = head_dim) in TMEM;
 //   a softmax thread owns one streamed row (TMEM lane) of the tile, forms P and dS in fp32
-//   and writes them as bf16 rows of 64 to shared memory (128-byte swizzle);
-//   acc0^T += Xs^T dS (dq^T or dk^T), and on the key side acc1^T += Ys^T P (dv^T):
+//   and writes them as bf16 rows of 64 to shared memory (128-byte swizzle; the one rounding
+//   the tensor cores' operands need);
+//   acc0^T += Xs^T dS (dq^T or dk^T), and for a key item acc1^T += Ys^T P (dv^T):
 //   M = head_dim (MN-major A: the streamed tile as it lies), N = 64 (MN-major B), K = 128.
 // M is 128 in every product at head_dim 128 (M = 64 issues at half rate).
 //
@@ -33,9 +33,15 @@
 // a list does not have read as zeros: every box has the same size and no row of a tile is
 // ever stale. Rows that are not there get P = dS = 0.
 //
-// Warps: 0 loads, 1 issues MMAs, 2 owns TMEM, 4-11 are two softmax warpgroups that take the
-// tiles in turn, so one tile's exponentials run under the other's products. Every wait is
-// bounded, as in the forward kernel.
+// One persistent CTA per SM takes query items, then key items, from two counters (which CTA
+// takes an item changes no sum), so neither side has a last wave of its own. A key item is only
+// some eight tiles long, so its boundaries must not drain the pipeline: roles run through the
+// items independently, the loads of the next item start while the last one's sums are still
+// formed, and accumulators are double-buffered in TMEM. Roles (16 warps):
+//   0 Xs, X0, Y0 loads and the item counter; 1 Ys loads and row statistics (two issuing warps:
+//   one alone reaches half the SM's ingest rate); 2 score products; 3 accumulating products;
+//   4-11 two softmax warpgroups, tiles in turn; 12-15 epilogue.
+// Every wait is bounded, as in the forward kernel.
 #include "lf_attn_bwd.h"
 #include "lf_device.cuh"
 
@@ -46,16 +52,20 @@
 namespace lf {
 namespace {
 
-constexpr int BWD_THREADS = 384;
-constexpr int W_LOAD = 0, W_MMA = 1, W_TMEM = 2, W_SOFT0 = 4;
-constexpr uint32_t TMEM_COLS = 512;  // S' of warpgroup g: 64 g; dP': 128 + 64 g; acc0^T: 256; acc1^T: 320
-constexpr uint32_t TM_DP = 128, TM_ACC0 = 256, TM_ACC1 = 320;
+constexpr int BWD_THREADS = 512;
+constexpr int W_LOADX = 0, W_LOADY = 1, W_SCORE = 2, W_ACC = 3, W_SOFT0 = 4, W_EPI0 = 12;
+constexpr int SCHED_READERS = 15;           // every warp but the one that publishes items
+constexpr uint32_t TMEM_COLS = 512;         // S' of tile t: 64 (t % 2); dP': 128 more;
+constexpr uint32_t TM_DP = 128;             // acc0^T of the n-th item with tiles: 256 + 128 (n % 2), acc1^T 64 more
+constexpr uint32_t TM_ACC = 256;
 
 template <int D, bool KV>
 struct BwdLayout {
     static constexpr int NP = D / 64;                       // 64-element panels of a row
-    static constexpr int NX = D == 64 ? 4 : (KV ? 2 : 3);   // tiles in the Xs and Ys rings: Ys is only read
-    static constexpr int NY = D == 64 ? 4 : 2;              // by dP' on the query side and leaves early
+    // tiles in the Xs and Ys rings (a query item's Ys is only read by dP' and leaves early; it
+    // needs no P buffers, so a third Xs tile fits)
+    static constexpr int NX = D == 64 ? 4 : (KV ? 2 : 3);
+    static constexpr int NY = D == 64 ? 4 : 2;
     static constexpr uint32_t OWN_PANEL = 64u * 128u;
     static constexpr uint32_t OWN = NP * OWN_PANEL;
     static constexpr uint32_t PANEL = 128u * 128u;
@@ -63,441 +73,678 @@ struct BwdLayout {
     static constexpr uint32_t PBUF = 128u * 128u;           // 128 rows x 64 bf16
     static constexpr uint32_t OFF_X0 = 0;
     static constexpr uint32_t OFF_Y0 = OFF_X0 + OWN;
-    static constexpr uint32_t OFF_X = OFF_Y0 + OWN;
+    static constexpr uint32_t OFF_DS = OFF_Y0 + OWN;
+    static constexpr uint32_t OFF_X = OFF_DS + 2 * PBUF;
     static constexpr uint32_t OFF_Y = OFF_X + NX * TILE;
-    static constexpr uint32_t OFF_DS = OFF_Y + NY * TILE;
-    static constexpr uint32_t OFF_P = OFF_DS + 2 * PBUF;    // key side only
-    static constexpr uint32_t OFF_AUX = OFF_P + (KV ? 2 * PBUF : 0u);
+    static constexpr uint32_t OFF_P = OFF_Y + NY * TILE;    // key items only
+    static constexpr uint32_t END = OFF_P + (KV ? 2 * PBUF : 0u);
 };
 
-struct BwdAux {
-    uint64_t own_full;
+struct BwdBars {
+    uint64_t own_full, own_empty;
     uint64_t x_full[4], x_empty[4], y_full[4], y_empty[4];
-    uint64_t s_full[2], p_full[2], p_empty[2];
-    uint64_t done;
+    uint64_t s_full[2], s_free[2], p_full[2], p_empty[2];
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t info_full[2], info_empty[2];
+    uint64_t sched_full[4], sched_empty[4];
+    uint64_t drain_s, drain_a;
+};
+
+template <int D>
+struct BwdAux {
+    BwdBars bars[2];  // query items, key items: a barrier is initialised once
     uint32_t tmem_base;
     int abort;
-    alignas(16) float lse2[64];   // query side: log2(e) lse of the CTA's rows (+inf where P must be 0)
-    alignas(16) float delta[64];
+    int sched_item[4], sched_cnt[4];  // item -1: no more
+    int tile_rows[4][2];              // query side: valid rows of an Xs slot's two blocks
+    // minus log2(e) lse (-inf: P = 0) and minus delta; query side: the item's 64 rows by item
+    // parity; key side: an Ys slot's 128 rows
+    alignas(16) float info[D == 64 ? 4 : 2][2][128];
 };
 
-template <int D, bool KV>
+template <int D>
 constexpr uint32_t bwd_smem_bytes()
 {
-    return BwdLayout<D, KV>::OFF_AUX + static_cast<uint32_t>(sizeof(BwdAux)) + 1024u;
+    constexpr uint32_t q = BwdLayout<D, false>::END, k = BwdLayout<D, true>::END;
+    return (q > k ? q : k) + static_cast<uint32_t>(sizeof(BwdAux<D>));
 }
 
-// A row's log-sum-exp in base 2; +inf (P = 0) for a row that attends to nothing.
-__device__ __forceinline__ float lse_log2(float lse)
+// Minus a row's log-sum-exp in base 2; -inf (P = 0) for a row that attends to nothing.
+__device__ __forceinline__ float neg_lse_log2(float lse)
 {
-    return lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
+    return lse == -INFINITY ? -INFINITY : lse * -1.4426950408889634f;
 }
 
-template <int D, bool KV>
-__global__ void __launch_bounds__(BWD_THREADS, 1)
-attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_x0, const __grid_constant__ CUtensorMap tm_y0,
-                const __grid_constant__ CUtensorMap tm_xs, const __grid_constant__ CUtensorMap tm_ys, const AttnBwdArgs a)
+// (d0, d1) = (a0 * b + c0, a1 * b + c1), packed
+__device__ __forceinline__ void ffma2_s(float& d0, float& d1, float a0, float a1, float b, float c0, float c1)
 {
-    using L = BwdLayout<D, KV>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    BwdAux& x = *reinterpret_cast<BwdAux*>(smem + L::OFF_AUX);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\t"
+        "mov.b64 rb, {%4, %4};\n\t"
+        "mov.b64 rc, {%5, %6};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\t"
+        "mov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
+}
 
-    // This CTA's block: frame f0, block j0 of it; n0 valid rows starting at out_row of the output.
-    const int per_head = KV ? a.Nkv : a.Rq;
-    const int bh = blockIdx.x / per_head;
-    const int own = blockIdx.x - bh * per_head;
-    const int f0 = own / a.bpf, j0 = own - f0 * a.bpf;
-    const int n0 = j0 == a.bpf - 1 ? a.rem : 64;
-    const long long head_row = static_cast<long long>(bh) * (KV ? a.kv_stride : a.Lq);
-    const long long out_row = head_row + static_cast<long long>(f0) * a.F + j0 * 64;
-    const long long lrow = static_cast<long long>(bh) * per_head + own;
-    const int* lst = KV ? a.row_list + lrow * a.Rq : a.block_list + lrow * a.list_cap;
-    int cnt = KV ? a.row_count[lrow] : __ldg(a.block_count + lrow);
+// A query item's count, clamped as the forward clamps it.
+template <bool KV>
+__device__ __forceinline__ int item_count(const AttnBwdArgs& a, int item)
+{
+    int cnt = KV ? a.row_count[item] : __ldg(a.block_count + item);
     if (!KV && (cnt < 0 || cnt > a.list_cap)) {
-        if (tid == 0) record_error(a.err, DEVERR_LIST | 1);
+        record_error(a.err, DEVERR_LIST | 1);
         cnt = cnt < 0 ? 0 : a.list_cap;
     }
-    const int n_it = (cnt + 1) >> 1;
-    const int listed = KV ? a.Rq : a.Nkv;       // valid ids are [0, listed)
-    const int frames = KV ? a.n_cur : a.NF;     // frames of the streamed side
+    return cnt;
+}
 
-    if (tid == 0) {
-        mbar_init(&x.own_full, 1);
-        for (int s = 0; s < 4; ++s) {
-            mbar_init(&x.x_full[s], 1);
-            mbar_init(&x.x_empty[s], 1);
-            mbar_init(&x.y_full[s], 1);
-            mbar_init(&x.y_empty[s], 1);
+struct Own {  // an item's own block
+    int bh, f, j, n;       // head, frame, block of the frame, valid rows
+    long long row;         // its first row in the output
+    const int* list;
+};
+
+template <bool KV>
+__device__ __forceinline__ Own own_of(const AttnBwdArgs& a, int item)
+{
+    const int per_head = KV ? a.Nkv : a.Rq;
+    Own o;
+    o.bh = item / per_head;
+    const int g = item - o.bh * per_head;
+    o.f = g / a.bpf;
+    o.j = g - o.f * a.bpf;
+    o.n = o.j == a.bpf - 1 ? a.rem : 64;
+    o.row = static_cast<long long>(o.bh) * (KV ? a.kv_stride : a.Lq) + static_cast<long long>(o.f) * a.F + o.j * 64;
+    o.list = KV ? a.row_list + static_cast<long long>(item) * a.Rq : a.block_list + static_cast<long long>(item) * a.list_cap;
+    return o;
+}
+
+// One side's items, every role. Returns when the CTA has no more (or aborts).
+template <int D, bool KV>
+__device__ __forceinline__ void run_side(const CUtensorMap* tm_x0, const CUtensorMap* tm_y0, const CUtensorMap* tm_xs,
+                                         const CUtensorMap* tm_ys, const AttnBwdArgs& a, uint8_t* smem, BwdAux<D>& x)
+{
+    using L = BwdLayout<D, KV>;
+    BwdBars& m = x.bars[KV ? 1 : 0];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t tmem = x.tmem_base;
+    volatile int* abort_flag = &x.abort;
+    const int n_items = a.BH * (KV ? a.Nkv : a.Rq);
+    const int listed = KV ? a.Rq : a.Nkv;      // valid ids are [0, listed)
+    const int frames = KV ? a.n_cur : a.NF;    // frames of the streamed side
+    const int list_len = KV ? a.Rq : a.list_cap;
+
+    // The k-th published item; false: no more, or aborting.
+    int k = 0, item = 0, cnt = 0;
+    auto next_item = [&]() -> bool {
+        const int s = k & 3;
+        if (!mbar_wait(&m.sched_full[s], (k >> 2) & 1, abort_flag, a.err, 0x42)) return false;
+        item = x.sched_item[s];
+        cnt = x.sched_cnt[s];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m.sched_empty[s]);
+        ++k;
+        return item >= 0;
+    };
+
+    if (warp == W_LOADX) {
+        // Items are claimed one ahead, and their count and first ids loaded while the one before streams.
+        auto claim = [&]() { return lane == 0 ? atomicAdd(a.next_item + (KV ? 1 : 0), 1) : 0; };
+        int nitem = __shfl_sync(0xffffffffu, claim(), 0), ncnt = 0, nids = -1;
+        auto look = [&]() {
+            if (nitem < n_items) {
+                ncnt = item_count<KV>(a, nitem);
+                nids = lane < list_len ? __ldg(own_of<KV>(a, nitem).list + lane) : -1;
+            }
+        };
+        look();
+        int t = 0, ne = 0;  // tiles and items with tiles so far
+        int armed_x = 0, armed_own = 0;
+        bool ok = true;
+        while (ok) {
+            const bool more = nitem < n_items;
+            item = nitem;
+            cnt = ncnt;
+            int ids = nids;
+            const int s = k & 3;
+            if (!mbar_wait(&m.sched_empty[s], ((k >> 2) & 1) ^ 1, abort_flag, a.err, 0x43)) break;
+            if (lane == 0) {
+                x.sched_item[s] = more ? item : -1;
+                x.sched_cnt[s] = cnt;
+            }
+            __syncwarp();
+            mbar_arrive_elect(&m.sched_full[s]);
+            ++k;
+            if (!more) break;
+            const int claimed = claim();
+            const Own o = own_of<KV>(a, item);
+            const int n_it = (cnt + 1) >> 1;
+            if (n_it > 0) {
+                if (!KV) {
+                    const int b = ne & 1;
+                    if (!mbar_wait(&m.info_empty[b], ((ne >> 1) & 1) ^ 1, abort_flag, a.err, 0x44)) break;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int r = lane + 32 * i;
+                        x.info[b][0][r] = r < o.n ? neg_lse_log2(__ldg(a.lse + o.row + r)) : -INFINITY;
+                        x.info[b][1][r] = r < o.n ? -a.delta[o.row + r] : 0.f;
+                    }
+                    __syncwarp();
+                    mbar_arrive_elect(&m.info_full[b]);
+                }
+                if (!mbar_wait(&m.own_empty, (ne & 1) ^ 1, abort_flag, a.err, 0x45)) break;
+                mbar_arrive_expect_tx_elect(&m.own_full, 2 * L::OWN);
+                for (int p = 0; p < L::NP; ++p) {
+                    tma_load_4d_elect(smem + L::OFF_X0 + p * L::OWN_PANEL, tm_x0, p * 64, o.j * 64, o.f, o.bh, &m.own_full);
+                    tma_load_4d_elect(smem + L::OFF_Y0 + p * L::OWN_PANEL, tm_y0, p * 64, o.j * 64, o.f, o.bh, &m.own_full);
+                }
+                armed_own = ++ne;
+            }
+            for (int it = 0; it < n_it; ++it, ++t) {
+                if (it > 0 && (it & 15) == 0) {
+                    const int e = 2 * it + lane;
+                    ids = e < cnt ? __ldg(o.list + e) : -1;
+                }
+                int tau[2], tok[2], rows[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int e = 2 * it + h;
+                    const int id = __shfl_sync(0xffffffffu, ids, e & 31);
+                    const bool good = e < cnt && id >= 0 && id < listed;
+                    if (e < cnt && !good && lane == 0) record_error(a.err, DEVERR_LIST | 2);
+                    tau[h] = good ? id / a.bpf : frames;  // past the last frame: the box reads zeros
+                    const int j = good ? id - tau[h] * a.bpf : 0;
+                    tok[h] = j * 64;
+                    rows[h] = good ? (j == a.bpf - 1 ? a.rem : 64) : 0;
+                }
+                const int xi = t % L::NX;
+                if (!(ok = mbar_wait(&m.x_empty[xi], ((t / L::NX) & 1) ^ 1, abort_flag, a.err, 0x46))) break;
+                if (!KV && lane == 0) {
+                    x.tile_rows[xi][0] = rows[0];
+                    x.tile_rows[xi][1] = rows[1];
+                }
+                __syncwarp();
+                mbar_arrive_expect_tx_elect(&m.x_full[xi], L::TILE);
+                for (int h = 0; h < 2; ++h)
+                    for (int p = 0; p < L::NP; ++p)
+                        tma_load_4d_elect(smem + L::OFF_X + xi * L::TILE + p * L::PANEL + h * 8192u, tm_xs, p * 64, tok[h],
+                                          tau[h], o.bh, &m.x_full[xi]);
+                armed_x = t + 1;
+                if (it == 0) {
+                    nitem = __shfl_sync(0xffffffffu, claimed, 0);
+                    look();
+                }
+            }
+            if (n_it == 0) {
+                nitem = __shfl_sync(0xffffffffu, claimed, 0);
+                look();
+            }
         }
-        for (int g = 0; g < 2; ++g) {
-            mbar_init(&x.s_full[g], 1);
-            mbar_init(&x.p_full[g], 4);  // one arrival per warp of the warpgroup
-            mbar_init(&x.p_empty[g], 1);
+        if (*abort_flag) {  // let every copy already issued land
+            if (armed_own > 0) mbar_drain(&m.own_full, (armed_own - 1) & 1, 10000000ull);
+            for (int e = max(0, armed_x - L::NX); e < armed_x; ++e)
+                mbar_drain(&m.x_full[e % L::NX], (e / L::NX) & 1, 10000000ull);
         }
-        mbar_init(&x.done, 1);
-        x.abort = 0;
+    } else if (warp == W_LOADY) {
+        int t = 0;
+        bool ok = true;
+        while (ok && next_item()) {
+            const Own o = own_of<KV>(a, item);
+            const int n_it = (cnt + 1) >> 1;
+            int ids = lane < cnt ? __ldg(o.list + lane) : -1;
+            // key side: lse and delta of the lane's four rows of a tile, loaded a tile ahead
+            float l4[4], d4[4];
+            auto stats = [&](int it) {
+                if (!KV || it >= n_it) return;
+                const int e = 2 * it + (lane >> 4), r0 = (lane & 15) * 4;
+                const int id = __shfl_sync(0xffffffffu, ids, e & 31);
+                int rows = 0;
+                long long at = 0;
+                if (e < cnt && id >= 0 && id < listed) {
+                    const int f = id / a.bpf, j = id - f * a.bpf;
+                    rows = j == a.bpf - 1 ? a.rem : 64;
+                    at = static_cast<long long>(o.bh) * a.Lq + f * a.F + j * 64 + r0;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bool there = r0 + i < rows;
+                    l4[i] = there ? __ldg(a.lse + at + i) : -INFINITY;
+                    d4[i] = there ? a.delta[at + i] : 0.f;
+                }
+            };
+            stats(0);
+            for (int it = 0; it < n_it; ++it, ++t) {
+                int tau[2], tok[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int e = 2 * it + h;
+                    const int id = __shfl_sync(0xffffffffu, ids, e & 31);
+                    const bool good = e < cnt && id >= 0 && id < listed;
+                    tau[h] = good ? id / a.bpf : frames;
+                    tok[h] = good ? (id - tau[h] * a.bpf) * 64 : 0;
+                }
+                const int yi = t % L::NY;
+                if (!(ok = mbar_wait(&m.y_empty[yi], ((t / L::NY) & 1) ^ 1, abort_flag, a.err, 0x47))) break;
+                if (KV) {
+                    *reinterpret_cast<float4*>(&x.info[yi][0][lane * 4]) =
+                        make_float4(neg_lse_log2(l4[0]), neg_lse_log2(l4[1]), neg_lse_log2(l4[2]), neg_lse_log2(l4[3]));
+                    *reinterpret_cast<float4*>(&x.info[yi][1][lane * 4]) = make_float4(-d4[0], -d4[1], -d4[2], -d4[3]);
+                }
+                __syncwarp();
+                mbar_arrive_expect_tx_elect(&m.y_full[yi], L::TILE);
+                for (int h = 0; h < 2; ++h)
+                    for (int p = 0; p < L::NP; ++p)
+                        tma_load_4d_elect(smem + L::OFF_Y + yi * L::TILE + p * L::PANEL + h * 8192u, tm_ys, p * 64, tok[h],
+                                          tau[h], o.bh, &m.y_full[yi]);
+                if ((it & 15) == 15) {
+                    const int e = 2 * (it + 1) + lane;
+                    ids = e < cnt ? __ldg(o.list + e) : -1;
+                }
+                stats(it + 1);
+            }
+        }
+        if (*abort_flag)
+            for (int e = max(0, t - L::NY); e < t; ++e) mbar_drain(&m.y_full[e % L::NY], (e / L::NY) & 1, 10000000ull);
+    } else if (warp == W_SCORE) {
+        constexpr uint32_t IDESC = idesc_bf16_f32(128, 64, false, false);
+        const uint64_t dX0 = sdesc_sw128(smem_u32(smem + L::OFF_X0), 16, 1024);
+        const uint64_t dY0 = sdesc_sw128(smem_u32(smem + L::OFF_Y0), 16, 1024);
+        const uint64_t dX = sdesc_sw128(smem_u32(smem + L::OFF_X), 16, 1024);
+        const uint64_t dY = sdesc_sw128(smem_u32(smem + L::OFF_Y), 16, 1024);
+        int t = 0, ne = 0;
+        bool ok = true;
+        while (ok && next_item()) {
+            const int n_it = (cnt + 1) >> 1;
+            if (n_it == 0) continue;
+            if (!mbar_wait(&m.own_full, ne & 1, abort_flag, a.err, 0x50)) break;
+            for (int it = 0; it < n_it; ++it, ++t) {
+                const int xi = t % L::NX, yi = t % L::NY, b = t & 1, u = t >> 1;
+                const uint32_t d = tmem + 64u * static_cast<uint32_t>(b);
+                if (!(ok = mbar_wait(&m.s_free[b], (u & 1) ^ 1, abort_flag, a.err, 0x51))) break;
+                if (!(ok = mbar_wait(&m.x_full[xi], (t / L::NX) & 1, abort_flag, a.err, 0x52))) break;
+                tc_fence_after();  // the softmax's TMEM reads of this buffer come first
+                const uint64_t xb = dX + ((xi * L::TILE) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    umma_bf16_elect(d, xb + (((kk >> 2) * L::PANEL + (kk & 3) * 32) >> 4),
+                                    dX0 + (((kk >> 2) * L::OWN_PANEL + (kk & 3) * 32) >> 4), IDESC, kk > 0 ? 1u : 0u);
+                if (!(ok = mbar_wait(&m.y_full[yi], (t / L::NY) & 1, abort_flag, a.err, 0x53))) break;
+                const uint64_t yb = dY + ((yi * L::TILE) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    umma_bf16_elect(d + TM_DP, yb + (((kk >> 2) * L::PANEL + (kk & 3) * 32) >> 4),
+                                    dY0 + (((kk >> 2) * L::OWN_PANEL + (kk & 3) * 32) >> 4), IDESC, kk > 0 ? 1u : 0u);
+                if (!KV) umma_commit_elect(&m.y_empty[yi]);
+                umma_commit_elect(&m.s_full[b]);
+            }
+            if (ok) umma_commit_elect(&m.own_empty);
+            ++ne;
+        }
+        if (*abort_flag) {
+            umma_commit_elect(&m.drain_s);
+            mbar_drain(&m.drain_s, 0, 10000000ull);
+        }
+    } else if (warp == W_ACC) {
+        constexpr uint32_t IDESC = idesc_bf16_f32(D, 64, true, true);
+        const uint64_t dX = sdesc_sw128(smem_u32(smem + L::OFF_X), L::PANEL, 1024);
+        const uint64_t dY = sdesc_sw128(smem_u32(smem + L::OFF_Y), L::PANEL, 1024);
+        const uint64_t dDS = sdesc_sw128(smem_u32(smem + L::OFF_DS), 1024, 1024);
+        const uint64_t dP = sdesc_sw128(smem_u32(smem + L::OFF_P), 1024, 1024);
+        int t = 0, ne = 0;
+        bool ok = true;
+        while (ok && next_item()) {
+            const int n_it = (cnt + 1) >> 1;
+            if (n_it == 0) continue;
+            const int e = ne & 1;
+            if (!mbar_wait(&m.acc_empty[e], ((ne >> 1) & 1) ^ 1, abort_flag, a.err, 0x54)) break;
+            tc_fence_after();  // the epilogue's reads of these accumulators come first
+            const uint32_t acc = tmem + TM_ACC + 128u * static_cast<uint32_t>(e);
+            for (int it = 0; it < n_it; ++it, ++t) {
+                const int xi = t % L::NX, yi = t % L::NY, b = t & 1;
+                if (!(ok = mbar_wait(&m.x_full[xi], (t / L::NX) & 1, abort_flag, a.err, 0x55))) break;
+                if (KV && !(ok = mbar_wait(&m.y_full[yi], (t / L::NY) & 1, abort_flag, a.err, 0x56))) break;
+                if (!(ok = mbar_wait(&m.p_full[b], (t >> 1) & 1, abort_flag, a.err, 0x57))) break;
+                tc_fence_after();
+                const uint64_t xb = dX + ((xi * L::TILE) >> 4), yb = dY + ((yi * L::TILE) >> 4);
+                const uint64_t sb = dDS + ((b * L::PBUF) >> 4), pb = dP + ((b * L::PBUF) >> 4);
+                const int slices = 2 * it + 1 < cnt ? 8 : 4;  // 16 rows each; the second block may be missing
+                for (int kk = 0; kk < slices; ++kk) {
+                    const uint32_t more = (it > 0 || kk > 0) ? 1u : 0u;
+                    umma_bf16_elect(acc, xb + ((kk * 2048) >> 4), sb + ((kk * 2048) >> 4), IDESC, more);
+                    if (KV) umma_bf16_elect(acc + 64u, yb + ((kk * 2048) >> 4), pb + ((kk * 2048) >> 4), IDESC, more);
+                }
+                umma_commit_elect(&m.x_empty[xi]);
+                if (KV) umma_commit_elect(&m.y_empty[yi]);
+                umma_commit_elect(&m.p_empty[b]);
+            }
+            if (ok) umma_commit_elect(&m.acc_full[e]);
+            ++ne;
+        }
+        if (*abort_flag) {
+            umma_commit_elect(&m.drain_a);
+            mbar_drain(&m.drain_a, 0, 10000000ull);
+        }
+    } else if (warp < W_EPI0) {
+        // ---------------------------------------------------------------- softmax
+        const int g = (warp - W_SOFT0) >> 2;       // this warpgroup takes the tiles t % 2 == g
+        const int sp = warp & 3;                   // TMEM sub-partition
+        const int rr = sp * 32 + lane;             // streamed row of the tile
+        const uint32_t s_addr = tmem + (static_cast<uint32_t>(sp * 32) << 16) + 64u * g;
+        uint8_t* ds_row = smem + L::OFF_DS + g * L::PBUF + rr * 128;
+        uint8_t* p_row = smem + L::OFF_P + g * L::PBUF + rr * 128;
+        int t = 0, ne = 0;
+        bool ok = true;
+        while (ok && next_item()) {
+            const int n_it = (cnt + 1) >> 1;
+            if (n_it == 0) continue;
+            const int e = ne & 1;
+            const int t_end = t + n_it;
+            if (!KV && !(ok = mbar_wait(&m.info_full[e], (ne >> 1) & 1, abort_flag, a.err, 0x60))) break;
+            t += (t ^ g) & 1;                      // this warpgroup's first tile of the item
+            for (; t < t_end; t += 2) {
+                const int xi = t % L::NX, yi = t % L::NY, u = t >> 1;
+                float nl = 0.f, nd = 0.f;
+                bool valid = true;
+                if (KV) {
+                    if (!(ok = mbar_wait(&m.y_full[yi], (t / L::NY) & 1, abort_flag, a.err, 0x61))) break;
+                    nl = x.info[yi][0][rr];
+                    nd = x.info[yi][1][rr];
+                } else {
+                    if (!(ok = mbar_wait(&m.x_full[xi], (t / L::NX) & 1, abort_flag, a.err, 0x62))) break;
+                    valid = (rr & 63) < x.tile_rows[xi][rr >> 6];
+                }
+                if (!(ok = mbar_wait(&m.s_full[g], u & 1, abort_flag, a.err, 0x63))) break;
+                if (!(ok = mbar_wait(&m.p_empty[g], (u & 1) ^ 1, abort_flag, a.err, 0x64))) break;
+                __syncwarp();
+                tc_fence_after();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float sv[32], dp[32];
+                    tmem_ld32(s_addr + 32u * h, sv);
+                    tmem_ld32(s_addr + TM_DP + 32u * h, dp);
+                    tmem_ld_wait();
+                    if (h == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&m.s_free[g]);
+                    }
+#pragma unroll
+                    for (int c8 = 0; c8 < 4; ++c8) {
+                        uint32_t pk[4], dk[4];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const int c = 8 * c8 + 4 * q;
+                            float4 l4, d4;
+                            if (KV) {
+                                l4 = make_float4(nl, nl, nl, nl);
+                                d4 = make_float4(nd, nd, nd, nd);
+                            } else {
+                                l4 = *reinterpret_cast<const float4*>(&x.info[e][0][32 * h + c]);
+                                d4 = *reinterpret_cast<const float4*>(&x.info[e][1][32 * h + c]);
+                            }
+                            float e0, e1, e2, e3;
+                            ffma2_s(e0, e1, sv[c], sv[c + 1], a.scale_log2, l4.x, l4.y);
+                            ffma2_s(e2, e3, sv[c + 2], sv[c + 3], a.scale_log2, l4.z, l4.w);
+                            e0 = fast_exp2(e0);
+                            e1 = fast_exp2(e1);
+                            e2 = fast_exp2(e2);
+                            e3 = fast_exp2(e3);
+                            if (KV) {
+                                pk[2 * q] = pack_bf16x2(e0, e1);
+                                pk[2 * q + 1] = pack_bf16x2(e2, e3);
+                            }
+                            fadd2_acc(dp[c], dp[c + 1], d4.x, d4.y);
+                            fadd2_acc(dp[c + 2], dp[c + 3], d4.z, d4.w);
+                            fmul2(e0, e1, dp[c], dp[c + 1]);
+                            fmul2(e2, e3, dp[c + 2], dp[c + 3]);
+                            // a streamed key that is not there contributes nothing, whatever its P came out as
+                            // (a streamed query that is not there has P = 0)
+                            dk[2 * q] = KV || valid ? pack_bf16x2(e0, e1) : 0u;
+                            dk[2 * q + 1] = KV || valid ? pack_bf16x2(e2, e3) : 0u;
+                        }
+                        const int chunk = (4 * h + c8) ^ (rr & 7);
+                        *reinterpret_cast<uint4*>(ds_row + chunk * 16) = make_uint4(dk[0], dk[1], dk[2], dk[3]);
+                        if (KV) *reinterpret_cast<uint4*>(p_row + chunk * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&m.p_full[g]);
+            }
+            t = t_end;
+            if (!KV && ok) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&m.info_empty[e]);
+            }
+            ++ne;
+        }
+    } else {
+        // ---------------------------------------------------------------- epilogue
+        // acc^T [head_dim lanes][64 columns] -> bf16 rows. Neighbouring lanes (head_dim elements)
+        // swap one of each two columns, so that a lane stores two elements of one row.
+        const int sp = warp & 3;
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(sp * 32) << 16);
+        const int d = D == 128 ? sp * 32 + lane : sp * 16 + (lane & 15);  // M = 64: 16 rows in each sub-partition's first lanes
+        const bool has = D == 128 || lane < 16;
+        const bool odd = lane & 1;
+        int ne = 0;
+        while (next_item()) {
+            const Own o = own_of<KV>(a, item);
+            if (cnt == 0) {
+                constexpr int CH = D / 8;
+                for (int i = (warp - W_EPI0) * 32 + lane; i < o.n * CH; i += 128) {
+                    const long long at = o.row * D + i * 8;
+                    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4*>((KV ? a.dk : a.dq) + at) = z;
+                    if (KV) *reinterpret_cast<uint4*>(a.dv + at) = z;
+                }
+                continue;
+            }
+            const int e = ne & 1;
+            if (!mbar_wait(&m.acc_full[e], (ne >> 1) & 1, abort_flag, a.err, 0x65)) break;
+            ++ne;
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < (KV ? 4 : 2); ++q) {  // acc0 columns 0-31, 32-63, then acc1's
+                float v[32];
+                __syncwarp();
+                tmem_ld32(lane_base + TM_ACC + 128u * e + 32u * q, v);
+                tmem_ld_wait();
+                if (q == (KV ? 3 : 1)) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&m.acc_empty[e]);
+                }
+                const float f = q < 2 ? a.scale : 1.f;
+                uint16_t* dst = (KV ? (q < 2 ? a.dk : a.dv) : a.dq) + o.row * D + (d & ~1);
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                    const float keep = odd ? v[c + 1] : v[c], give = odd ? v[c] : v[c + 1];
+                    const float got = __shfl_xor_sync(0xffffffffu, give, 1);
+                    const int row = 32 * (q & 1) + c + (odd ? 1 : 0);
+                    const uint32_t w = odd ? pack_bf16x2(got * f, keep * f) : pack_bf16x2(keep * f, got * f);
+                    if (has && row < o.n) *reinterpret_cast<uint32_t*>(dst + static_cast<long long>(row) * D) = w;
+                }
+            }
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(BWD_THREADS, 1)
+attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_dout,
+                const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                const __grid_constant__ AttnBwdArgs a)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];  // 128-byte swizzled tiles want 1024-byte boundaries
+    constexpr uint32_t Q = BwdLayout<D, false>::END, K = BwdLayout<D, true>::END;
+    BwdAux<D>& x = *reinterpret_cast<BwdAux<D>*>(smem + (Q > K ? Q : K));
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int side = 0; side < 2; ++side) {
+            BwdBars& m = x.bars[side];
+            mbar_init(&m.own_full, 1);
+            mbar_init(&m.own_empty, 1);
+            for (int s = 0; s < 4; ++s) {
+                mbar_init(&m.x_full[s], 1);
+                mbar_init(&m.x_empty[s], 1);
+                mbar_init(&m.y_full[s], 1);
+                mbar_init(&m.y_empty[s], 1);
+                mbar_init(&m.sched_full[s], 1);
+                mbar_init(&m.sched_empty[s], SCHED_READERS);
+            }
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&m.s_full[b], 1);
+                mbar_init(&m.s_free[b], 4);      // one arrival per warp of the warpgroup
+                mbar_init(&m.p_full[b], 4);
+                mbar_init(&m.p_empty[b], 1);
+                mbar_init(&m.acc_full[b], 1);
+                mbar_init(&m.acc_empty[b], 4);   // the epilogue's warps
+                mbar_init(&m.info_full[b], 1);
+                mbar_init(&m.info_empty[b], 8);  // the softmax warps
+            }
+            mbar_init(&m.drain_s, 1);
+            mbar_init(&m.drain_a, 1);
+        }
+        x.abort = (smem_u32(smem) & 1023u) != 0;
+        if (x.abort) record_error(a.err, DEVERR_TIMEOUT | 0x7f);
         fence_mbar_init();
     }
-    if (warp == W_TMEM) {
+    if (warp == W_SCORE) {
         tmem_alloc(&x.tmem_base, TMEM_COLS);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = x.tmem_base;
-    volatile int* abort_flag = &x.abort;
-
-    if (warp == W_LOAD) {
-        if (n_it > 0) {
-            mbar_arrive_expect_tx_elect(&x.own_full, 2 * L::OWN);
-            for (int p = 0; p < L::NP; ++p) {
-                tma_load_4d_elect(smem + L::OFF_X0 + p * L::OWN_PANEL, &tm_x0, p * 64, j0 * 64, f0, bh, &x.own_full);
-                tma_load_4d_elect(smem + L::OFF_Y0 + p * L::OWN_PANEL, &tm_y0, p * 64, j0 * 64, f0, bh, &x.own_full);
-            }
-        }
-        int armed = 0;
-        for (int it = 0; it < n_it; ++it) {
-            int tau[2], tok[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int e = 2 * it + h;
-                const int id = e < cnt ? __ldg(lst + e) : -1;
-                const bool good = id >= 0 && id < listed;
-                if (e < cnt && !good && lane == 0) record_error(a.err, DEVERR_LIST | 2);
-                tau[h] = good ? id / a.bpf : frames;  // past the last frame: the box reads zeros
-                tok[h] = good ? (id - tau[h] * a.bpf) * 64 : 0;
-            }
-            const int xi = it % L::NX, yi = it % L::NY;
-            if (!mbar_wait(&x.x_empty[xi], ((it / L::NX) & 1) ^ 1, abort_flag, a.err, 0x40)) break;
-            mbar_arrive_expect_tx_elect(&x.x_full[xi], L::TILE);
-            for (int h = 0; h < 2; ++h)
-                for (int p = 0; p < L::NP; ++p)
-                    tma_load_4d_elect(smem + L::OFF_X + xi * L::TILE + p * L::PANEL + h * 8192u, &tm_xs, p * 64,
-                                          tok[h], tau[h], bh, &x.x_full[xi]);
-            armed = 2 * it + 1;
-            if (!mbar_wait(&x.y_empty[yi], ((it / L::NY) & 1) ^ 1, abort_flag, a.err, 0x41)) break;
-            mbar_arrive_expect_tx_elect(&x.y_full[yi], L::TILE);
-            for (int h = 0; h < 2; ++h)
-                for (int p = 0; p < L::NP; ++p)
-                    tma_load_4d_elect(smem + L::OFF_Y + yi * L::TILE + p * L::PANEL + h * 8192u, &tm_ys, p * 64,
-                                          tok[h], tau[h], bh, &x.y_full[yi]);
-            armed = 2 * it + 2;
-        }
-        if (*abort_flag && n_it > 0) {
-            // let every copy already issued land before the CTA exits
-            mbar_drain(&x.own_full, 0, 10000000ull);
-            const int xs = (armed + 1) >> 1, ys = armed >> 1;
-            for (int e = max(0, xs - L::NX); e < xs; ++e) mbar_drain(&x.x_full[e % L::NX], (e / L::NX) & 1, 10000000ull);
-            for (int e = max(0, ys - L::NY); e < ys; ++e) mbar_drain(&x.y_full[e % L::NY], (e / L::NY) & 1, 10000000ull);
-        }
-    } else if (warp == W_MMA) {
-        constexpr uint32_t IDESC_S = idesc_bf16_f32(128, 64, false, false);
-        constexpr uint32_t IDESC_A = idesc_bf16_f32(D, 64, true, true);
-        const uint64_t dX0 = sdesc_sw128(smem_u32(smem + L::OFF_X0), 16, 1024);
-        const uint64_t dY0 = sdesc_sw128(smem_u32(smem + L::OFF_Y0), 16, 1024);
-        const uint64_t dXk = sdesc_sw128(smem_u32(smem + L::OFF_X), 16, 1024);            // K-major: S'
-        const uint64_t dYk = sdesc_sw128(smem_u32(smem + L::OFF_Y), 16, 1024);
-        const uint64_t dXm = sdesc_sw128(smem_u32(smem + L::OFF_X), L::PANEL, 1024);      // MN-major: acc0
-        const uint64_t dYm = sdesc_sw128(smem_u32(smem + L::OFF_Y), L::PANEL, 1024);
-        const uint64_t dDS = sdesc_sw128(smem_u32(smem + L::OFF_DS), 1024, 1024);
-        const uint64_t dP = sdesc_sw128(smem_u32(smem + L::OFF_P), 1024, 1024);
-        bool ok = n_it > 0 && mbar_wait(&x.own_full, 0, abort_flag, a.err, 0x50);
-        bool issued = false;
-        // S' and dP' of tile it into warpgroup it & 1's buffers (its reads of tile it - 2 came
-        // before p_full of that tile, which acc(it - 2) waited for)
-        auto scores = [&](int it) -> bool {
-            const int xi = it % L::NX, yi = it % L::NY;
-            const uint32_t d = tmem + 64u * static_cast<uint32_t>(it & 1);
-            if (!mbar_wait(&x.x_full[xi], (it / L::NX) & 1, abort_flag, a.err, 0x51)) return false;
-            tc_fence_after();
-            const uint64_t xb = dXk + ((xi * L::TILE) >> 4);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-                umma_bf16_elect(d, xb + (((kk >> 2) * L::PANEL + (kk & 3) * 32) >> 4),
-                                dX0 + (((kk >> 2) * L::OWN_PANEL + (kk & 3) * 32) >> 4), IDESC_S, kk > 0 ? 1u : 0u);
-            issued = true;
-            if (!mbar_wait(&x.y_full[yi], (it / L::NY) & 1, abort_flag, a.err, 0x52)) return false;
-            const uint64_t yb = dYk + ((yi * L::TILE) >> 4);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-                umma_bf16_elect(d + TM_DP, yb + (((kk >> 2) * L::PANEL + (kk & 3) * 32) >> 4),
-                                dY0 + (((kk >> 2) * L::OWN_PANEL + (kk & 3) * 32) >> 4), IDESC_S, kk > 0 ? 1u : 0u);
-            if (!KV) umma_commit_elect(&x.y_empty[yi]);
-            umma_commit_elect(&x.s_full[it & 1]);
-            return true;
-        };
-        auto accumulate = [&](int it) -> bool {
-            const int g = it & 1, xi = it % L::NX, yi = it % L::NY;
-            if (!mbar_wait(&x.p_full[g], (it >> 1) & 1, abort_flag, a.err, 0x53)) return false;
-            tc_fence_after();
-            const uint64_t xb = dXm + ((xi * L::TILE) >> 4), yb = dYm + ((yi * L::TILE) >> 4);
-            const uint64_t sb = dDS + ((g * L::PBUF) >> 4), pb = dP + ((g * L::PBUF) >> 4);
-            const int slices = 2 * it + 1 < cnt ? 8 : 4;  // 16 rows each; the second block may be missing
-            for (int kk = 0; kk < slices; ++kk) {
-                const uint32_t more = (it > 0 || kk > 0) ? 1u : 0u;
-                umma_bf16_elect(tmem + TM_ACC0, xb + ((kk * 2048) >> 4), sb + ((kk * 2048) >> 4), IDESC_A, more);
-                if (KV) umma_bf16_elect(tmem + TM_ACC1, yb + ((kk * 2048) >> 4), pb + ((kk * 2048) >> 4), IDESC_A, more);
-            }
-            umma_commit_elect(&x.x_empty[xi]);
-            if (KV) umma_commit_elect(&x.y_empty[yi]);
-            umma_commit_elect(&x.p_empty[g]);
-            return true;
-        };
-        for (int it = 0; ok && it < n_it; ++it) {
-            ok = scores(it);
-            if (ok && it > 0) ok = accumulate(it - 1);
-        }
-        if (ok && n_it > 0) ok = accumulate(n_it - 1);
-        if (ok || issued) umma_commit_elect(&x.done);
-        if (*abort_flag && issued) mbar_drain(&x.done, 0, 10000000ull);
-    } else if (warp >= W_SOFT0) {
-        const int g = (warp - W_SOFT0) >> 2;       // this warpgroup takes the tiles it % 2 == g
-        const int sp = warp & 3;                   // TMEM sub-partition
-        const int rr = sp * 32 + lane;             // streamed row of the tile
-        const int hb = rr >> 6, ri = rr & 63;      // its block in the tile and row of the block
-        const uint32_t lane_base = tmem + (static_cast<uint32_t>(sp * 32) << 16);
-        const int st = tid - W_SOFT0 * 32;         // 0 .. 255
-
-        if (!KV) {
-            // delta of the CTA's 64 rows, eight rows a warp; the key side reads it from memory
-            constexpr int EPL = D / 32;
-            for (int i = 0; i < 8; ++i) {
-                const int r = (warp - W_SOFT0) * 8 + i;
-                float dot = 0.f;
-                if (r < n0) {
-                    const long long at = (out_row + r) * D + lane * EPL;
-                    uint32_t o[EPL / 2], d[EPL / 2], lo[EPL / 2] = {};
-                    if constexpr (EPL == 4) {
-                        if (a.out_lo) {
-                            const uint2 lu = __ldg(reinterpret_cast<const uint2*>(a.out_lo + at));
-                            lo[0] = lu.x; lo[1] = lu.y;
-                        }
-                        const uint2 ou = __ldg(reinterpret_cast<const uint2*>(a.out + at));
-                        const uint2 du = __ldg(reinterpret_cast<const uint2*>(a.dout + at));
-                        o[0] = ou.x; o[1] = ou.y; d[0] = du.x; d[1] = du.y;
-                    } else {
-                        if (a.out_lo) lo[0] = __ldg(reinterpret_cast<const uint32_t*>(a.out_lo + at));
-                        o[0] = __ldg(reinterpret_cast<const uint32_t*>(a.out + at));
-                        d[0] = __ldg(reinterpret_cast<const uint32_t*>(a.dout + at));
-                    }
-#pragma unroll
-                    for (int k = 0; k < EPL / 2; ++k) {
-                        dot = fmaf(__uint_as_float(o[k] << 16) + __uint_as_float(lo[k] << 16), __uint_as_float(d[k] << 16), dot);
-                        dot = fmaf(__uint_as_float(o[k] & 0xFFFF0000u) + __uint_as_float(lo[k] & 0xFFFF0000u),
-                                   __uint_as_float(d[k] & 0xFFFF0000u), dot);
-                    }
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-                if (lane == 0) {
-                    x.delta[r] = dot;
-                    x.lse2[r] = r < n0 ? lse_log2(__ldg(a.lse + out_row + r)) : INFINITY;
-                    if (r < n0) a.delta[out_row + r] = dot;
-                }
-            }
-            named_bar_sync(3, 256);
-        }
-
-        // The streamed row of tile `it`: is it there, and (key side) its lse and delta.
-        float lse2 = INFINITY, delta = 0.f, lse2_next = INFINITY, delta_next = 0.f;
-        bool valid = false, valid_next = false;
-        auto fetch = [&](int it) {
-            const int e = 2 * it + hb;
-            valid_next = false;
-            lse2_next = INFINITY;
-            delta_next = 0.f;
-            if (it < n_it && e < cnt) {
-                const int id = __ldg(lst + e);
-                if (id >= 0 && id < listed) {
-                    const int f = id / a.bpf, j = id - f * a.bpf;
-                    valid_next = ri < (j == a.bpf - 1 ? a.rem : 64);
-                    if (KV && valid_next) {
-                        const long long at = static_cast<long long>(bh) * a.Lq + f * a.F + j * 64 + ri;
-                        lse2_next = lse_log2(__ldg(a.lse + at));
-                        delta_next = a.delta[at];
-                    }
-                }
-            }
-        };
-        fetch(g);
-        int j = 0;
-        for (int it = g; it < n_it; it += 2, ++j) {
-            valid = valid_next;
-            lse2 = lse2_next;
-            delta = delta_next;
-            fetch(it + 2);
-            mbar_wait(&x.s_full[g], j & 1, abort_flag, a.err, 0x60);
-            __syncwarp();
-            tc_fence_after();
-            if (j > 0) mbar_wait(&x.p_empty[g], (j - 1) & 1, abort_flag, a.err, 0x61);
-            uint8_t* ds_row = smem + L::OFF_DS + g * L::PBUF + rr * 128;
-            uint8_t* p_row = smem + L::OFF_P + g * L::PBUF + rr * 128;
-            __syncwarp();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float sv[32], dp[32];
-                tmem_ld32(lane_base + 64u * g + 32u * h, sv);
-                tmem_ld32(lane_base + TM_DP + 64u * g + 32u * h, dp);
-                tmem_ld_wait();
-                uint32_t pk[16], dk[16];
-#pragma unroll
-                for (int c = 0; c < 32; c += 4) {
-                    float4 l4, d4;
-                    if (KV) {
-                        l4 = make_float4(lse2, lse2, lse2, lse2);
-                        d4 = make_float4(delta, delta, delta, delta);
-                    } else {
-                        l4 = *reinterpret_cast<const float4*>(&x.lse2[32 * h + c]);
-                        d4 = *reinterpret_cast<const float4*>(&x.delta[32 * h + c]);
-                    }
-                    const float p0 = fast_exp2(fmaf(sv[c], a.scale_log2, -l4.x));
-                    const float p1 = fast_exp2(fmaf(sv[c + 1], a.scale_log2, -l4.y));
-                    const float p2 = fast_exp2(fmaf(sv[c + 2], a.scale_log2, -l4.z));
-                    const float p3 = fast_exp2(fmaf(sv[c + 3], a.scale_log2, -l4.w));
-                    if (KV) {
-                        pk[c >> 1] = pack_bf16x2(p0, p1);
-                        pk[(c >> 1) + 1] = pack_bf16x2(p2, p3);
-                    }
-                    dk[c >> 1] = pack_bf16x2(p0 * (dp[c] - d4.x), p1 * (dp[c + 1] - d4.y));
-                    dk[(c >> 1) + 1] = pack_bf16x2(p2 * (dp[c + 2] - d4.z), p3 * (dp[c + 3] - d4.w));
-                }
-                // a streamed row that is not there contributes nothing, whatever its P came out as
-                if (!valid) {
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        dk[c] = 0u;
-                        if (KV) pk[c] = 0u;
-                    }
-                }
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int chunk = (4 * h + c) ^ (rr & 7);
-                    *reinterpret_cast<uint4*>(ds_row + chunk * 16) = make_uint4(dk[4 * c], dk[4 * c + 1], dk[4 * c + 2], dk[4 * c + 3]);
-                    if (KV)
-                        *reinterpret_cast<uint4*>(p_row + chunk * 16) = make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
-                }
-            }
-            fence_proxy_async_smem();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&x.p_full[g]);
-        }
-
-        // Epilogue: acc^T [head_dim lanes][64 columns] -> bf16 rows through shared memory (the Xs
-        // ring is idle once every MMA is done). Warpgroup g takes columns [32 g, 32 g + 32).
-        constexpr int NOUT = KV ? 2 : 1;
-        __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(smem + L::OFF_X);
-        if (n_it > 0) {
-            mbar_wait(&x.done, 0, abort_flag, a.err, 0x62);
-            __syncwarp();
-            tc_fence_after();
-            const int d = D == 128 ? rr : sp * 16 + (lane & 15);  // M = 64: 16 rows in each sub-partition's first lanes
-            const bool has = D == 128 || lane < 16;
-#pragma unroll
-            for (int o = 0; o < NOUT; ++o) {
-                float v[32];
-                __syncwarp();
-                tmem_ld32(lane_base + (o == 0 ? TM_ACC0 : TM_ACC1) + 32u * g, v);
-                tmem_ld_wait();
-                const float f = o == 0 ? a.scale : 1.f;
-                if (has) {
-#pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        stage[(o * 64 + 32 * g + c) * D + d] = __float2bfloat16_rn(v[c] * f);
-                }
-            }
-            tc_fence_before();
-            named_bar_sync(3, 256);
-        }
-        constexpr int CH = D / 8;  // 16-byte chunks of a row
-        for (int i = st; i < NOUT * n0 * CH; i += 256) {
-            const int o = i / (n0 * CH), q = i - o * (n0 * CH);
-            const int row = q / CH, c8 = q - row * CH;
-            uint16_t* dst = KV ? (o == 0 ? a.dk : a.dv) : a.dq;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (n_it > 0) v = *reinterpret_cast<const uint4*>(stage + (o * 64 + row) * D + c8 * 8);
-            *reinterpret_cast<uint4*>(dst + (out_row + row) * D + c8 * 8) = v;
-        }
-    }
+    if (!x.abort) run_side<D, false>(&tm_q, &tm_dout, &tm_k, &tm_v, a, smem, x);
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == W_TMEM) {
+    tc_fence_after();
+    if (!x.abort) run_side<D, true>(&tm_k, &tm_v, &tm_q, &tm_dout, a, smem, x);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == W_SCORE) {
         tc_fence_after();
-        tmem_dealloc(tmem, TMEM_COLS);
+        tmem_dealloc(x.tmem_base, TMEM_COLS);
     }
 }
 
-// Transposes the block lists of one head: for each KV block the query blocks that list it,
-// ascending. A CTA owns 1024 KV blocks and walks the head's rows 32 at a time: each row's
-// warp sets its bit for every block it lists, then each block's thread appends the bits it
-// finds. (Bits are set atomically, but the set does not depend on the order.)
-constexpr int TR_BLOCKS = 1024;
+// The gradient's preparation, one launch: the first CTAs transpose the block lists, the others
+// form delta.
+//
+// Transposition: for each KV block the query blocks that list it, ascending. A CTA owns 128 KV
+// blocks of a head and walks the head's rows 256 at a time: each row's warp sets its bit for
+// every block it lists, then each block's thread appends the bits it finds. (Bits are set
+// atomically, but the set does not depend on the order.) 128 blocks a CTA spread the scattered
+// stores of the lists over the machine; every CTA reads all lists of its head, from L2.
+//
+// Delta: <dout, out + out_lo> per row, a warp takes four rows at once.
+constexpr int PREP_THREADS = 512;
+constexpr int TR_BLOCKS = 128, TR_WORDS = 8;
+constexpr int DELTA_ROWS = 4 * (PREP_THREADS / 32);
 
-__global__ void __launch_bounds__(TR_BLOCKS) transpose_lists_kernel(const AttnBwdArgs a)
+template <int D>
+__global__ void __launch_bounds__(PREP_THREADS) attn_bwd_prep_kernel(const AttnBwdArgs a, int transposing)
 {
-    __shared__ uint32_t bits[TR_BLOCKS];
-    const int chunks = (a.Nkv + TR_BLOCKS - 1) / TR_BLOCKS;
-    const int bh = blockIdx.x / chunks, g0 = (blockIdx.x - bh * chunks) * TR_BLOCKS, t = threadIdx.x;
-    const int warp = t >> 5, lane = t & 31;
-    int n = 0;
-    int* mine = a.row_list + (static_cast<long long>(bh) * a.Nkv + g0 + t) * a.Rq;
-    for (int w = 0; w * 32 < a.Rq; ++w) {
-        bits[t] = 0u;
-        __syncthreads();
-        const int r = w * 32 + warp;
-        if (r < a.Rq) {
-            const long long lrow = static_cast<long long>(bh) * a.Rq + r;
-            const int cnt = min(max(__ldg(a.block_count + lrow), 0), a.list_cap);
-            const int* lst = a.block_list + lrow * a.list_cap;
-            for (int e = lane; e < cnt; e += 32) {
-                const int at = __ldg(lst + e) - g0;
-                if (at >= 0 && at < TR_BLOCKS && at + g0 < a.Nkv) {
-                    const uint32_t old = atomicOr(&bits[at], 1u << warp);
-                    if (old >> warp & 1u) record_error(a.err, DEVERR_LIST | 3);  // a block named twice
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    if (static_cast<int>(blockIdx.x) < transposing) {
+        __shared__ uint32_t bits[TR_WORDS][TR_BLOCKS];
+        if (blockIdx.x == 0 && t < 2) a.next_item[t] = 0;
+        const int chunks = (a.Nkv + TR_BLOCKS - 1) / TR_BLOCKS;
+        const int bh = blockIdx.x / chunks, g0 = (blockIdx.x - bh * chunks) * TR_BLOCKS;
+        const int g1 = min(TR_BLOCKS, a.Nkv - g0);
+        int n = 0;
+        int* mine = a.row_list + (static_cast<long long>(bh) * a.Nkv + g0 + t) * a.Rq;
+        for (int r0 = 0; r0 < a.Rq; r0 += 32 * TR_WORDS) {
+            for (int i = t; i < TR_WORDS * TR_BLOCKS; i += PREP_THREADS) bits[i / TR_BLOCKS][i % TR_BLOCKS] = 0u;
+            __syncthreads();
+            for (int r = r0 + warp; r < min(a.Rq, r0 + 32 * TR_WORDS); r += PREP_THREADS / 32) {
+                const long long lrow = static_cast<long long>(bh) * a.Rq + r;
+                const int cnt = min(max(__ldg(a.block_count + lrow), 0), a.list_cap);
+                const int* lst = a.block_list + lrow * a.list_cap;
+                const uint32_t bit = 1u << (r & 31);
+                uint32_t* word = bits[(r - r0) >> 5];
+                for (int e = lane; e < cnt; e += 32) {
+                    const int at = __ldg(lst + e) - g0;
+                    if (at >= 0 && at < g1 && (atomicOr(word + at, bit) & bit))
+                        record_error(a.err, DEVERR_LIST | 3);  // a block named twice
                 }
             }
+            __syncthreads();
+            if (t < TR_BLOCKS)
+                for (int w = 0; w < TR_WORDS; ++w)
+                    for (uint32_t m = bits[w][t]; m; m &= m - 1) mine[n++] = r0 + 32 * w + __ffs(m) - 1;
+            __syncthreads();
         }
-        __syncthreads();
-        for (uint32_t m = bits[t]; m; m &= m - 1) mine[n++] = w * 32 + __ffs(m) - 1;
-        __syncthreads();
+        if (t < g1) a.row_count[static_cast<long long>(bh) * a.Nkv + g0 + t] = n;
+        return;
     }
-    if (g0 + t < a.Nkv) a.row_count[static_cast<long long>(bh) * a.Nkv + g0 + t] = n;
-}
-
-template <int D, bool KV>
-cudaError_t launch_side(const AttnBwdMaps& m, const AttnBwdArgs& a, cudaStream_t s)
-{
-    constexpr uint32_t smem = bwd_smem_bytes<D, KV>();
-    static_assert(smem <= 232448, "shared memory plan exceeds 227 KB");
-    static std::atomic<bool> configured[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64 || !configured[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(attn_bwd_kernel<D, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_release);
+    constexpr int EPL = D / 32, W = EPL / 2;  // elements and words of a row a lane holds
+    const long long rows = static_cast<long long>(a.BH) * a.Lq;
+    const long long r0 = static_cast<long long>(blockIdx.x - transposing) * DELTA_ROWS + warp * 4;
+    uint32_t o[4][W], d[4][W], lo[4][W];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const long long at = (r0 + i) * D + lane * EPL;
+#pragma unroll
+        for (int w = 0; w < W; ++w) o[i][w] = d[i][w] = lo[i][w] = 0u;
+        if (r0 + i < rows) {
+            if constexpr (W == 2) {
+                *reinterpret_cast<uint2*>(o[i]) = __ldg(reinterpret_cast<const uint2*>(a.out + at));
+                *reinterpret_cast<uint2*>(d[i]) = __ldg(reinterpret_cast<const uint2*>(a.dout + at));
+                if (a.out_lo) *reinterpret_cast<uint2*>(lo[i]) = __ldg(reinterpret_cast<const uint2*>(a.out_lo + at));
+            } else {
+                o[i][0] = __ldg(reinterpret_cast<const uint32_t*>(a.out + at));
+                d[i][0] = __ldg(reinterpret_cast<const uint32_t*>(a.dout + at));
+                if (a.out_lo) lo[i][0] = __ldg(reinterpret_cast<const uint32_t*>(a.out_lo + at));
+            }
+        }
     }
-    const unsigned grid = static_cast<unsigned>(a.BH) * static_cast<unsigned>(KV ? a.Nkv : a.Rq);
-    if (KV)
-        attn_bwd_kernel<D, KV><<<grid, BWD_THREADS, smem, s>>>(m.k, m.v, m.q, m.dout, a);
-    else
-        attn_bwd_kernel<D, KV><<<grid, BWD_THREADS, smem, s>>>(m.q, m.dout, m.k, m.v, a);
-    return cudaGetLastError();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float dot = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            dot = fmaf(__uint_as_float(o[i][w] << 16) + __uint_as_float(lo[i][w] << 16), __uint_as_float(d[i][w] << 16), dot);
+            dot = fmaf(__uint_as_float(o[i][w] & 0xFFFF0000u) + __uint_as_float(lo[i][w] & 0xFFFF0000u),
+                       __uint_as_float(d[i][w] & 0xFFFF0000u), dot);
+        }
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, s);
+        if (lane == 0 && r0 + i < rows) a.delta[r0 + i] = dot;
+    }
 }
 
 template <int D>
 cudaError_t launch_d(const AttnBwdMaps& m, const AttnBwdArgs& a, cudaStream_t s)
 {
-    const unsigned chunks = static_cast<unsigned>((a.Nkv + TR_BLOCKS - 1) / TR_BLOCKS);
-    transpose_lists_kernel<<<chunks * static_cast<unsigned>(a.BH), TR_BLOCKS, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
+    constexpr uint32_t smem = bwd_smem_bytes<D>();
+    static_assert(smem <= 232448, "shared memory plan exceeds 227 KB");
+    static std::atomic<int> sms[64];  // SMs of a device once the kernel's shared memory is set there
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if ((e = launch_side<D, false>(m, a, s)) != cudaSuccess) return e;
-    return launch_side<D, true>(m, a, s);
+    int sm = dev >= 0 && dev < 64 ? sms[dev].load(std::memory_order_acquire) : 0;
+    if (sm == 0) {
+        e = cudaFuncSetAttribute(attn_bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+        if ((e = cudaDeviceGetAttribute(&sm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) sms[dev].store(sm, std::memory_order_release);
+    }
+    const int transposing = (a.Nkv + TR_BLOCKS - 1) / TR_BLOCKS * a.BH;
+    const long long rows = static_cast<long long>(a.BH) * a.Lq;
+    const unsigned prep = static_cast<unsigned>(transposing + (rows + DELTA_ROWS - 1) / DELTA_ROWS);
+    attn_bwd_prep_kernel<D><<<prep, PREP_THREADS, 0, s>>>(a, transposing);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const long long items = static_cast<long long>(a.BH) * (a.Rq + a.Nkv);
+    attn_bwd_kernel<D><<<static_cast<unsigned>(items < sm ? items : sm), BWD_THREADS, smem, s>>>(m.q, m.dout, m.k, m.v, a);
+    return cudaGetLastError();
 }
 
 }  // namespace

@@ -17,6 +17,7 @@ struct AttnBwdArgs {
     float* delta;    // [BH, Lq]: <dout, out> of each row
     int* row_list;   // [BH, Nkv, Rq]: the query blocks that list each KV block, ascending
     int* row_count;  // [BH, Nkv]
+    int* next_item;  // [2]: query and key items taken so far
     uint16_t* dq;
     uint16_t* dk;
     uint16_t* dv;
