@@ -40,7 +40,7 @@
 // formed, and accumulators are double-buffered in TMEM. Roles (16 warps):
 //   0 Xs, X0, Y0 loads and the item counter; 1 Ys loads and row statistics (two issuing warps:
 //   one alone reaches half the SM's ingest rate); 2 score products; 3 accumulating products;
-//   4-11 two softmax warpgroups, tiles in turn; 12-15 epilogue.
+//   4-11 two softmax warpgroups, half of every tile's columns each; 12-15 epilogue.
 // Every wait is bounded, as in the forward kernel.
 #include "lf_attn_bwd.h"
 #include "lf_device.cuh"
@@ -168,8 +168,11 @@ __device__ __forceinline__ void run_side(const CUtensorMap* tm_x0, const CUtenso
 {
     using L = BwdLayout<D, KV>;
     BwdBars& m = x.bars[KV ? 1 : 0];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t tmem = x.tmem_base;
+    // Values that steer a whole warp are taken through a shuffle: that tells the compiler that they
+    // are uniform, so that the MMA and copy issue keeps its operands in uniform registers (without
+    // it the key items took 650 us instead of 536 at layer480p).
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, x.tmem_base, 0);
     volatile int* abort_flag = &x.abort;
     const int n_items = a.BH * (KV ? a.Nkv : a.Rq);
     const int listed = KV ? a.Rq : a.Nkv;      // valid ids are [0, listed)
@@ -181,8 +184,8 @@ __device__ __forceinline__ void run_side(const CUtensorMap* tm_x0, const CUtenso
     auto next_item = [&]() -> bool {
         const int s = k & 3;
         if (!mbar_wait(&m.sched_full[s], (k >> 2) & 1, abort_flag, a.err, 0x42)) return false;
-        item = x.sched_item[s];
-        cnt = x.sched_cnt[s];
+        item = __shfl_sync(0xffffffffu, x.sched_item[s], 0);
+        cnt = __shfl_sync(0xffffffffu, x.sched_cnt[s], 0);
         __syncwarp();
         if (lane == 0) mbar_arrive(&m.sched_empty[s]);
         ++k;
@@ -363,20 +366,21 @@ __device__ __forceinline__ void run_side(const CUtensorMap* tm_x0, const CUtenso
                 const int xi = t % L::NX, yi = t % L::NY, b = t & 1, u = t >> 1;
                 const uint32_t d = tmem + 64u * static_cast<uint32_t>(b);
                 if (!(ok = mbar_wait(&m.s_free[b], (u & 1) ^ 1, abort_flag, a.err, 0x51))) break;
-                if (!(ok = mbar_wait(&m.x_full[xi], (t / L::NX) & 1, abort_flag, a.err, 0x52))) break;
+                // dP' first: Ys is released first, and so arrives first
+                if (!(ok = mbar_wait(&m.y_full[yi], (t / L::NY) & 1, abort_flag, a.err, 0x52))) break;
                 tc_fence_after();  // the softmax's TMEM reads of this buffer come first
-                const uint64_t xb = dX + ((xi * L::TILE) >> 4);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    umma_bf16_elect(d, xb + (((kk >> 2) * L::PANEL + (kk & 3) * 32) >> 4),
-                                    dX0 + (((kk >> 2) * L::OWN_PANEL + (kk & 3) * 32) >> 4), IDESC, kk > 0 ? 1u : 0u);
-                if (!(ok = mbar_wait(&m.y_full[yi], (t / L::NY) & 1, abort_flag, a.err, 0x53))) break;
                 const uint64_t yb = dY + ((yi * L::TILE) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
                     umma_bf16_elect(d + TM_DP, yb + (((kk >> 2) * L::PANEL + (kk & 3) * 32) >> 4),
                                     dY0 + (((kk >> 2) * L::OWN_PANEL + (kk & 3) * 32) >> 4), IDESC, kk > 0 ? 1u : 0u);
                 if (!KV) umma_commit_elect(&m.y_empty[yi]);
+                if (!(ok = mbar_wait(&m.x_full[xi], (t / L::NX) & 1, abort_flag, a.err, 0x53))) break;
+                const uint64_t xb = dX + ((xi * L::TILE) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    umma_bf16_elect(d, xb + (((kk >> 2) * L::PANEL + (kk & 3) * 32) >> 4),
+                                    dX0 + (((kk >> 2) * L::OWN_PANEL + (kk & 3) * 32) >> 4), IDESC, kk > 0 ? 1u : 0u);
                 umma_commit_elect(&m.s_full[b]);
             }
             if (ok) umma_commit_elect(&m.own_empty);
@@ -409,14 +413,26 @@ __device__ __forceinline__ void run_side(const CUtensorMap* tm_x0, const CUtenso
                 tc_fence_after();
                 const uint64_t xb = dX + ((xi * L::TILE) >> 4), yb = dY + ((yi * L::TILE) >> 4);
                 const uint64_t sb = dDS + ((b * L::PBUF) >> 4), pb = dP + ((b * L::PBUF) >> 4);
-                const int slices = 2 * it + 1 < cnt ? 8 : 4;  // 16 rows each; the second block may be missing
-                for (int kk = 0; kk < slices; ++kk) {
-                    const uint32_t more = (it > 0 || kk > 0) ? 1u : 0u;
-                    umma_bf16_elect(acc, xb + ((kk * 2048) >> 4), sb + ((kk * 2048) >> 4), IDESC, more);
-                    if (KV) umma_bf16_elect(acc + 64u, yb + ((kk * 2048) >> 4), pb + ((kk * 2048) >> 4), IDESC, more);
+                const uint32_t more = it > 0 ? 1u : 0u;
+                const bool both = 2 * it + 1 < cnt;  // the tile's second block (the last four slices of 16 rows) may be missing
+                if (KV) {  // dv first: Ys can be filled again while dk is summed
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_bf16_elect(acc + 64u, yb + ((kk * 2048) >> 4), pb + ((kk * 2048) >> 4), IDESC, kk > 0 ? 1u : more);
+                    if (both)
+#pragma unroll
+                        for (int kk = 4; kk < 8; ++kk)
+                            umma_bf16_elect(acc + 64u, yb + ((kk * 2048) >> 4), pb + ((kk * 2048) >> 4), IDESC, 1u);
+                    umma_commit_elect(&m.y_empty[yi]);
                 }
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_bf16_elect(acc, xb + ((kk * 2048) >> 4), sb + ((kk * 2048) >> 4), IDESC, kk > 0 ? 1u : more);
+                if (both)
+#pragma unroll
+                    for (int kk = 4; kk < 8; ++kk)
+                        umma_bf16_elect(acc, xb + ((kk * 2048) >> 4), sb + ((kk * 2048) >> 4), IDESC, 1u);
                 umma_commit_elect(&m.x_empty[xi]);
-                if (KV) umma_commit_elect(&m.y_empty[yi]);
                 umma_commit_elect(&m.p_empty[b]);
             }
             if (ok) umma_commit_elect(&m.acc_full[e]);
@@ -428,12 +444,12 @@ __device__ __forceinline__ void run_side(const CUtensorMap* tm_x0, const CUtenso
         }
     } else if (warp < W_EPI0) {
         // ---------------------------------------------------------------- softmax
-        const int g = (warp - W_SOFT0) >> 2;       // this warpgroup takes the tiles t % 2 == g
+        const int g = (warp - W_SOFT0) >> 2;       // this warpgroup takes columns [32 g, 32 g + 32) of every tile
         const int sp = warp & 3;                   // TMEM sub-partition
         const int rr = sp * 32 + lane;             // streamed row of the tile
-        const uint32_t s_addr = tmem + (static_cast<uint32_t>(sp * 32) << 16) + 64u * g;
-        uint8_t* ds_row = smem + L::OFF_DS + g * L::PBUF + rr * 128;
-        uint8_t* p_row = smem + L::OFF_P + g * L::PBUF + rr * 128;
+        const uint32_t s_addr = tmem + (static_cast<uint32_t>(sp * 32) << 16) + 32u * g;
+        uint8_t* ds_row = smem + L::OFF_DS + rr * 128;
+        uint8_t* p_row = smem + L::OFF_P + rr * 128;
         int t = 0, ne = 0;
         bool ok = true;
         while (ok && next_item()) {
@@ -442,9 +458,8 @@ __device__ __forceinline__ void run_side(const CUtensorMap* tm_x0, const CUtenso
             const int e = ne & 1;
             const int t_end = t + n_it;
             if (!KV && !(ok = mbar_wait(&m.info_full[e], (ne >> 1) & 1, abort_flag, a.err, 0x60))) break;
-            t += (t ^ g) & 1;                      // this warpgroup's first tile of the item
-            for (; t < t_end; t += 2) {
-                const int xi = t % L::NX, yi = t % L::NY, u = t >> 1;
+            for (; t < t_end; ++t) {
+                const int xi = t % L::NX, yi = t % L::NY, b = t & 1, u = t >> 1;
                 float nl = 0.f, nd = 0.f;
                 bool valid = true;
                 if (KV) {
@@ -455,21 +470,18 @@ __device__ __forceinline__ void run_side(const CUtensorMap* tm_x0, const CUtenso
                     if (!(ok = mbar_wait(&m.x_full[xi], (t / L::NX) & 1, abort_flag, a.err, 0x62))) break;
                     valid = (rr & 63) < x.tile_rows[xi][rr >> 6];
                 }
-                if (!(ok = mbar_wait(&m.s_full[g], u & 1, abort_flag, a.err, 0x63))) break;
-                if (!(ok = mbar_wait(&m.p_empty[g], (u & 1) ^ 1, abort_flag, a.err, 0x64))) break;
+                if (!(ok = mbar_wait(&m.s_full[b], u & 1, abort_flag, a.err, 0x63))) break;
+                if (!(ok = mbar_wait(&m.p_empty[b], (u & 1) ^ 1, abort_flag, a.err, 0x64))) break;
                 __syncwarp();
                 tc_fence_after();
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                {
                     float sv[32], dp[32];
-                    tmem_ld32(s_addr + 32u * h, sv);
-                    tmem_ld32(s_addr + TM_DP + 32u * h, dp);
+                    tmem_ld32(s_addr + 64u * b, sv);
+                    tmem_ld32(s_addr + TM_DP + 64u * b, dp);
                     tmem_ld_wait();
-                    if (h == 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&m.s_free[g]);
-                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&m.s_free[b]);
 #pragma unroll
                     for (int c8 = 0; c8 < 4; ++c8) {
                         uint32_t pk[4], dk[4];
@@ -481,8 +493,8 @@ __device__ __forceinline__ void run_side(const CUtensorMap* tm_x0, const CUtenso
                                 l4 = make_float4(nl, nl, nl, nl);
                                 d4 = make_float4(nd, nd, nd, nd);
                             } else {
-                                l4 = *reinterpret_cast<const float4*>(&x.info[e][0][32 * h + c]);
-                                d4 = *reinterpret_cast<const float4*>(&x.info[e][1][32 * h + c]);
+                                l4 = *reinterpret_cast<const float4*>(&x.info[e][0][32 * g + c]);
+                                d4 = *reinterpret_cast<const float4*>(&x.info[e][1][32 * g + c]);
                             }
                             float e0, e1, e2, e3;
                             ffma2_s(e0, e1, sv[c], sv[c + 1], a.scale_log2, l4.x, l4.y);
@@ -504,14 +516,14 @@ __device__ __forceinline__ void run_side(const CUtensorMap* tm_x0, const CUtenso
                             dk[2 * q] = KV || valid ? pack_bf16x2(e0, e1) : 0u;
                             dk[2 * q + 1] = KV || valid ? pack_bf16x2(e2, e3) : 0u;
                         }
-                        const int chunk = (4 * h + c8) ^ (rr & 7);
-                        *reinterpret_cast<uint4*>(ds_row + chunk * 16) = make_uint4(dk[0], dk[1], dk[2], dk[3]);
-                        if (KV) *reinterpret_cast<uint4*>(p_row + chunk * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                        const uint32_t at = b * L::PBUF + static_cast<uint32_t>(((4 * g + c8) ^ (rr & 7)) * 16);
+                        *reinterpret_cast<uint4*>(ds_row + at) = make_uint4(dk[0], dk[1], dk[2], dk[3]);
+                        if (KV) *reinterpret_cast<uint4*>(p_row + at) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
                     }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&m.p_full[g]);
+                if (lane == 0) mbar_arrive(&m.p_full[b]);
             }
             t = t_end;
             if (!KV && ok) {
@@ -598,13 +610,13 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             }
             for (int b = 0; b < 2; ++b) {
                 mbar_init(&m.s_full[b], 1);
-                mbar_init(&m.s_free[b], 4);      // one arrival per warp of the warpgroup
-                mbar_init(&m.p_full[b], 4);
+                mbar_init(&m.s_free[b], 8);      // the softmax warps
+                mbar_init(&m.p_full[b], 8);
                 mbar_init(&m.p_empty[b], 1);
                 mbar_init(&m.acc_full[b], 1);
                 mbar_init(&m.acc_empty[b], 4);   // the epilogue's warps
                 mbar_init(&m.info_full[b], 1);
-                mbar_init(&m.info_empty[b], 8);  // the softmax warps
+                mbar_init(&m.info_empty[b], 8);
             }
             mbar_init(&m.drain_s, 1);
             mbar_init(&m.drain_a, 1);
