@@ -66,22 +66,27 @@ struct BwdLayout {
     // needs no P buffers, so a third Xs tile fits)
     static constexpr int NX = D == 64 ? 4 : (KV ? 2 : 3);
     static constexpr int NY = D == 64 ? 4 : 2;
+    // Key items are short, so the next item's X0 and Y0 load while the last one's tiles are still at
+    // work (790 -> 767 us at layer480p); the room comes from second P and dS buffers, which two
+    // tiles in flight hardly use.
+    static constexpr int OWNS = KV ? 2 : 1;
+    static constexpr int PBUFS = KV ? 1 : 2;
     static constexpr uint32_t OWN_PANEL = 64u * 128u;
     static constexpr uint32_t OWN = NP * OWN_PANEL;
     static constexpr uint32_t PANEL = 128u * 128u;
     static constexpr uint32_t TILE = NP * PANEL;
     static constexpr uint32_t PBUF = 128u * 128u;           // 128 rows x 64 bf16
     static constexpr uint32_t OFF_X0 = 0;
-    static constexpr uint32_t OFF_Y0 = OFF_X0 + OWN;
-    static constexpr uint32_t OFF_DS = OFF_Y0 + OWN;
-    static constexpr uint32_t OFF_X = OFF_DS + 2 * PBUF;
+    static constexpr uint32_t OFF_Y0 = OFF_X0 + OWN;        // an own buffer is X0, Y0
+    static constexpr uint32_t OFF_DS = OFF_X0 + OWNS * 2 * OWN;
+    static constexpr uint32_t OFF_X = OFF_DS + PBUFS * PBUF;
     static constexpr uint32_t OFF_Y = OFF_X + NX * TILE;
     static constexpr uint32_t OFF_P = OFF_Y + NY * TILE;    // key items only
-    static constexpr uint32_t END = OFF_P + (KV ? 2 * PBUF : 0u);
+    static constexpr uint32_t END = OFF_P + (KV ? PBUFS * PBUF : 0u);
 };
 
 struct BwdBars {
-    uint64_t own_full, own_empty;
+    uint64_t own_full[2], own_empty[2];
     uint64_t x_full[4], x_empty[4], y_full[4], y_empty[4];
     uint64_t s_full[2], s_free[2], p_full[2], p_empty[2];
     uint64_t acc_full[2], acc_empty[2];
@@ -237,11 +242,13 @@ __device__ __forceinline__ void run_side(const CUtensorMap* tm_x0, const CUtenso
                     __syncwarp();
                     mbar_arrive_elect(&m.info_full[b]);
                 }
-                if (!mbar_wait(&m.own_empty, (ne & 1) ^ 1, abort_flag, a.err, 0x45)) break;
-                mbar_arrive_expect_tx_elect(&m.own_full, 2 * L::OWN);
+                const int ob = ne % L::OWNS;
+                if (!mbar_wait(&m.own_empty[ob], ((ne / L::OWNS) & 1) ^ 1, abort_flag, a.err, 0x45)) break;
+                mbar_arrive_expect_tx_elect(&m.own_full[ob], 2 * L::OWN);
+                uint8_t* own = smem + L::OFF_X0 + ob * 2 * L::OWN;
                 for (int p = 0; p < L::NP; ++p) {
-                    tma_load_4d_elect(smem + L::OFF_X0 + p * L::OWN_PANEL, tm_x0, p * 64, o.j * 64, o.f, o.bh, &m.own_full);
-                    tma_load_4d_elect(smem + L::OFF_Y0 + p * L::OWN_PANEL, tm_y0, p * 64, o.j * 64, o.f, o.bh, &m.own_full);
+                    tma_load_4d_elect(own + p * L::OWN_PANEL, tm_x0, p * 64, o.j * 64, o.f, o.bh, &m.own_full[ob]);
+                    tma_load_4d_elect(own + L::OWN + p * L::OWN_PANEL, tm_y0, p * 64, o.j * 64, o.f, o.bh, &m.own_full[ob]);
                 }
                 armed_own = ++ne;
             }
@@ -286,7 +293,8 @@ __device__ __forceinline__ void run_side(const CUtensorMap* tm_x0, const CUtenso
             }
         }
         if (*abort_flag) {  // let every copy already issued land
-            if (armed_own > 0) mbar_drain(&m.own_full, (armed_own - 1) & 1, 10000000ull);
+            for (int n = max(0, armed_own - L::OWNS); n < armed_own; ++n)
+                mbar_drain(&m.own_full[n % L::OWNS], (n / L::OWNS) & 1, 10000000ull);
             for (int e = max(0, armed_x - L::NX); e < armed_x; ++e)
                 mbar_drain(&m.x_full[e % L::NX], (e / L::NX) & 1, 10000000ull);
         }
@@ -352,8 +360,7 @@ __device__ __forceinline__ void run_side(const CUtensorMap* tm_x0, const CUtenso
             for (int e = max(0, t - L::NY); e < t; ++e) mbar_drain(&m.y_full[e % L::NY], (e / L::NY) & 1, 10000000ull);
     } else if (warp == W_SCORE) {
         constexpr uint32_t IDESC = idesc_bf16_f32(128, 64, false, false);
-        const uint64_t dX0 = sdesc_sw128(smem_u32(smem + L::OFF_X0), 16, 1024);
-        const uint64_t dY0 = sdesc_sw128(smem_u32(smem + L::OFF_Y0), 16, 1024);
+        const uint64_t dOwn = sdesc_sw128(smem_u32(smem + L::OFF_X0), 16, 1024);
         const uint64_t dX = sdesc_sw128(smem_u32(smem + L::OFF_X), 16, 1024);
         const uint64_t dY = sdesc_sw128(smem_u32(smem + L::OFF_Y), 16, 1024);
         int t = 0, ne = 0;
@@ -361,7 +368,9 @@ __device__ __forceinline__ void run_side(const CUtensorMap* tm_x0, const CUtenso
         while (ok && next_item()) {
             const int n_it = (cnt + 1) >> 1;
             if (n_it == 0) continue;
-            if (!mbar_wait(&m.own_full, ne & 1, abort_flag, a.err, 0x50)) break;
+            const int ob = ne % L::OWNS;
+            if (!mbar_wait(&m.own_full[ob], (ne / L::OWNS) & 1, abort_flag, a.err, 0x50)) break;
+            const uint64_t dX0 = dOwn + ((ob * 2 * L::OWN) >> 4), dY0 = dX0 + (L::OWN >> 4);
             for (int it = 0; it < n_it; ++it, ++t) {
                 const int xi = t % L::NX, yi = t % L::NY, b = t & 1, u = t >> 1;
                 const uint32_t d = tmem + 64u * static_cast<uint32_t>(b);
@@ -383,7 +392,7 @@ __device__ __forceinline__ void run_side(const CUtensorMap* tm_x0, const CUtenso
                                     dX0 + (((kk >> 2) * L::OWN_PANEL + (kk & 3) * 32) >> 4), IDESC, kk > 0 ? 1u : 0u);
                 umma_commit_elect(&m.s_full[b]);
             }
-            if (ok) umma_commit_elect(&m.own_empty);
+            if (ok) umma_commit_elect(&m.own_empty[ob]);
             ++ne;
         }
         if (*abort_flag) {
@@ -412,7 +421,7 @@ __device__ __forceinline__ void run_side(const CUtensorMap* tm_x0, const CUtenso
                 if (!(ok = mbar_wait(&m.p_full[b], (t >> 1) & 1, abort_flag, a.err, 0x57))) break;
                 tc_fence_after();
                 const uint64_t xb = dX + ((xi * L::TILE) >> 4), yb = dY + ((yi * L::TILE) >> 4);
-                const uint64_t sb = dDS + ((b * L::PBUF) >> 4), pb = dP + ((b * L::PBUF) >> 4);
+                const uint64_t sb = dDS + (((b % L::PBUFS) * L::PBUF) >> 4), pb = dP + (((b % L::PBUFS) * L::PBUF) >> 4);
                 const uint32_t more = it > 0 ? 1u : 0u;
                 const bool both = 2 * it + 1 < cnt;  // the tile's second block (the last four slices of 16 rows) may be missing
                 if (KV) {  // dv first: Ys can be filled again while dk is summed
@@ -433,7 +442,7 @@ __device__ __forceinline__ void run_side(const CUtensorMap* tm_x0, const CUtenso
                     for (int kk = 4; kk < 8; ++kk)
                         umma_bf16_elect(acc, xb + ((kk * 2048) >> 4), sb + ((kk * 2048) >> 4), IDESC, 1u);
                 umma_commit_elect(&m.x_empty[xi]);
-                umma_commit_elect(&m.p_empty[b]);
+                umma_commit_elect(&m.p_empty[t % L::PBUFS]);
             }
             if (ok) umma_commit_elect(&m.acc_full[e]);
             ++ne;
@@ -471,55 +480,53 @@ __device__ __forceinline__ void run_side(const CUtensorMap* tm_x0, const CUtenso
                     valid = (rr & 63) < x.tile_rows[xi][rr >> 6];
                 }
                 if (!(ok = mbar_wait(&m.s_full[b], u & 1, abort_flag, a.err, 0x63))) break;
-                if (!(ok = mbar_wait(&m.p_empty[b], (u & 1) ^ 1, abort_flag, a.err, 0x64))) break;
                 __syncwarp();
                 tc_fence_after();
-                {
-                    float sv[32], dp[32];
-                    tmem_ld32(s_addr + 64u * b, sv);
-                    tmem_ld32(s_addr + TM_DP + 64u * b, dp);
-                    tmem_ld_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&m.s_free[b]);
+                float sv[32], dp[32];
+                tmem_ld32(s_addr + 64u * b, sv);
+                tmem_ld32(s_addr + TM_DP + 64u * b, dp);
+                tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&m.s_free[b]);
+                uint32_t pk[KV ? 16 : 1], dk[16];
 #pragma unroll
-                    for (int c8 = 0; c8 < 4; ++c8) {
-                        uint32_t pk[4], dk[4];
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const int c = 8 * c8 + 4 * q;
-                            float4 l4, d4;
-                            if (KV) {
-                                l4 = make_float4(nl, nl, nl, nl);
-                                d4 = make_float4(nd, nd, nd, nd);
-                            } else {
-                                l4 = *reinterpret_cast<const float4*>(&x.info[e][0][32 * g + c]);
-                                d4 = *reinterpret_cast<const float4*>(&x.info[e][1][32 * g + c]);
-                            }
-                            float e0, e1, e2, e3;
-                            ffma2_s(e0, e1, sv[c], sv[c + 1], a.scale_log2, l4.x, l4.y);
-                            ffma2_s(e2, e3, sv[c + 2], sv[c + 3], a.scale_log2, l4.z, l4.w);
-                            e0 = fast_exp2(e0);
-                            e1 = fast_exp2(e1);
-                            e2 = fast_exp2(e2);
-                            e3 = fast_exp2(e3);
-                            if (KV) {
-                                pk[2 * q] = pack_bf16x2(e0, e1);
-                                pk[2 * q + 1] = pack_bf16x2(e2, e3);
-                            }
-                            fadd2_acc(dp[c], dp[c + 1], d4.x, d4.y);
-                            fadd2_acc(dp[c + 2], dp[c + 3], d4.z, d4.w);
-                            fmul2(e0, e1, dp[c], dp[c + 1]);
-                            fmul2(e2, e3, dp[c + 2], dp[c + 3]);
-                            // a streamed key that is not there contributes nothing, whatever its P came out as
-                            // (a streamed query that is not there has P = 0)
-                            dk[2 * q] = KV || valid ? pack_bf16x2(e0, e1) : 0u;
-                            dk[2 * q + 1] = KV || valid ? pack_bf16x2(e2, e3) : 0u;
-                        }
-                        const uint32_t at = b * L::PBUF + static_cast<uint32_t>(((4 * g + c8) ^ (rr & 7)) * 16);
-                        *reinterpret_cast<uint4*>(ds_row + at) = make_uint4(dk[0], dk[1], dk[2], dk[3]);
-                        if (KV) *reinterpret_cast<uint4*>(p_row + at) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                for (int c = 0; c < 32; c += 4) {
+                    float4 l4, d4;
+                    if (KV) {
+                        l4 = make_float4(nl, nl, nl, nl);
+                        d4 = make_float4(nd, nd, nd, nd);
+                    } else {
+                        l4 = *reinterpret_cast<const float4*>(&x.info[e][0][32 * g + c]);
+                        d4 = *reinterpret_cast<const float4*>(&x.info[e][1][32 * g + c]);
                     }
+                    float e0, e1, e2, e3;
+                    ffma2_s(e0, e1, sv[c], sv[c + 1], a.scale_log2, l4.x, l4.y);
+                    ffma2_s(e2, e3, sv[c + 2], sv[c + 3], a.scale_log2, l4.z, l4.w);
+                    e0 = fast_exp2(e0);
+                    e1 = fast_exp2(e1);
+                    e2 = fast_exp2(e2);
+                    e3 = fast_exp2(e3);
+                    if constexpr (KV) {
+                        pk[c / 2] = pack_bf16x2(e0, e1);
+                        pk[c / 2 + 1] = pack_bf16x2(e2, e3);
+                    }
+                    fadd2_acc(dp[c], dp[c + 1], d4.x, d4.y);
+                    fadd2_acc(dp[c + 2], dp[c + 3], d4.z, d4.w);
+                    fmul2(e0, e1, dp[c], dp[c + 1]);
+                    fmul2(e2, e3, dp[c + 2], dp[c + 3]);
+                    // a streamed key that is not there contributes nothing, whatever its P came out as
+                    // (a streamed query that is not there has P = 0)
+                    dk[c / 2] = KV || valid ? pack_bf16x2(e0, e1) : 0u;
+                    dk[c / 2 + 1] = KV || valid ? pack_bf16x2(e2, e3) : 0u;
+                }
+                if (!(ok = mbar_wait(&m.p_empty[t % L::PBUFS], ((t / L::PBUFS) & 1) ^ 1, abort_flag, a.err, 0x64))) break;
+#pragma unroll
+                for (int c8 = 0; c8 < 4; ++c8) {
+                    const uint32_t at = (t % L::PBUFS) * L::PBUF + static_cast<uint32_t>(((4 * g + c8) ^ (rr & 7)) * 16);
+                    *reinterpret_cast<uint4*>(ds_row + at) = make_uint4(dk[4 * c8], dk[4 * c8 + 1], dk[4 * c8 + 2], dk[4 * c8 + 3]);
+                    if constexpr (KV)
+                        *reinterpret_cast<uint4*>(p_row + at) = make_uint4(pk[4 * c8], pk[4 * c8 + 1], pk[4 * c8 + 2], pk[4 * c8 + 3]);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -598,17 +605,17 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     if (threadIdx.x == 0) {
         for (int side = 0; side < 2; ++side) {
             BwdBars& m = x.bars[side];
-            mbar_init(&m.own_full, 1);
-            mbar_init(&m.own_empty, 1);
             for (int s = 0; s < 4; ++s) {
                 mbar_init(&m.x_full[s], 1);
                 mbar_init(&m.x_empty[s], 1);
-                mbar_init(&m.y_full[s], 1);
+                mbar_init(&m.y_full[s], 1);  // key side: the copies, and the rows' statistics
                 mbar_init(&m.y_empty[s], 1);
                 mbar_init(&m.sched_full[s], 1);
                 mbar_init(&m.sched_empty[s], SCHED_READERS);
             }
             for (int b = 0; b < 2; ++b) {
+                mbar_init(&m.own_full[b], 1);
+                mbar_init(&m.own_empty[b], 1);
                 mbar_init(&m.s_full[b], 1);
                 mbar_init(&m.s_free[b], 8);      // the softmax warps
                 mbar_init(&m.p_full[b], 8);
