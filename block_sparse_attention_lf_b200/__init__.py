@@ -31,6 +31,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional, Sequence, Tuple
 
@@ -275,17 +276,29 @@ def _dtype_code(dtype) -> int:
 
 def _sized_ptr(t, dtype, shape, device, name: str) -> int:
     """Address of a contiguous CUDA tensor of exactly this dtype and shape on ``device``."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _dev_ptr(t, dtype, name)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device.index != device:
-        raise ValueError(f"{name} must be on the current device (cuda:{device}), got {t.device}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be on the current device (cuda:{device}), got {t.device}")
 
 
 def _device() -> int:
     import torch
     return torch.cuda.current_device()
+
+
+def _raw_stream(stream, device: int) -> int:
+    """Handle of ``stream``, or of the device's current stream."""
+    if stream is None:
+        import torch
+        get = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without building a Stream object
+        return get(device) if get is not None else torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def lf_version() -> str:
@@ -503,7 +516,7 @@ def lf_block_sparse_attn_lse(shape: LfShape, q, k, v, block_list, block_count, l
         _sized_ptr(out, torch.bfloat16, q.shape, dev, "out"),
         None if out_lo is None else _sized_ptr(out_lo, torch.bfloat16, q.shape, dev, "out_lo"),
         _sized_ptr(lse, torch.float32, q.shape[:3], dev, "lse"), int(tail_pieces), ws, ws_bytes,
-        _stream(stream)), "lf_block_sparse_attn_lse")
+        _raw_stream(stream, dev)), "lf_block_sparse_attn_lse")
 
 
 def lf_attn_bwd_workspace(shape: LfShape) -> int:
@@ -527,7 +540,7 @@ def lf_block_sparse_attn_bwd(shape: LfShape, q, k, v, out, dout, lse, block_list
         _sized_ptr(dout, bf, q.shape, dev, "dout"), _sized_ptr(lse, torch.float32, q.shape[:3], dev, "lse"), lp, cp,
         list_cap, float(softmax_scale), _sized_ptr(dq, bf, q.shape, dev, "dq"),
         _sized_ptr(dk, bf, k.shape, dev, "dk"), _sized_ptr(dv, bf, k.shape, dev, "dv"),
-        _sized_ptr(workspace, torch.uint8, workspace.shape, dev, "workspace"), workspace.numel(), _stream(stream)),
+        _sized_ptr(workspace, torch.uint8, workspace.shape, dev, "workspace"), workspace.numel(), _raw_stream(stream, dev)),
         "lf_block_sparse_attn_bwd")
 
 
@@ -540,46 +553,64 @@ def lf_rope(plan: RopePlan, xs: Sequence, outs: Sequence, positions, rotate: Opt
     call's head-major tensors; an output may be its own input. ``positions``: int32
     [tokens, n_axes] or [batch, tokens, n_axes]. ``rotate[i]`` False copies tensor i. ``backward``:
     xs are gradients of the outputs, outs receive the gradients of the inputs."""
-    import torch
     n = len(xs)
     if len(outs) != n or not 1 <= n <= 3:
         raise ValueError("lf_rope takes one to three tensors and as many outputs")
-    dev, dtype = _device(), xs[0].dtype
-    B, _, T, D = xs[0].shape
+    dev, first = _device(), xs[0]
+    dtype = first.dtype
+    if first.dim() != 4:
+        raise ValueError("tensors must be [batch, heads, tokens, head_dim]")
+    B, _, T, D = first.shape
     if D != plan.head_dim:
         raise ValueError(f"tensors have head_dim {D}, the plan {plan.head_dim}")
-    io = (_RopeIo * n)()
+    io = b""
     for i in range(n):
         x, o = xs[i], outs[i]
-        for t, name in ((x, "x"), (o, "out")):
-            if not t.is_cuda:
-                raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-            if t.device.index != dev:
-                raise ValueError(f"{name} must be on the current device (cuda:{dev}), got {t.device}")
-            if t.dtype != dtype:
-                raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        shape, xst, ost = x.shape, x.stride(), o.stride()
+        if x.dtype is not dtype or o.dtype is not dtype or x.get_device() != dev or o.get_device() != dev:
+            _refuse_rope(x, o, dtype, dev)
+        shape = x.shape
         if len(shape) != 4 or shape[0] != B or shape[2] != T or shape[3] != D or o.shape != shape:
             raise ValueError("every tensor and its output must be [batch, heads, tokens, head_dim] of the same sizes")
-        if xst[3] != 1 or ost[3] != 1:
+        xb, xh, xt, xe = x.stride()
+        ob, oh, ot, oe = o.stride()
+        if xe != 1 or oe != 1:
             raise ValueError("the last dimension must have stride 1")
-        e = io[i]
-        e.x, e.out, e.heads, e.rotate = x.data_ptr(), o.data_ptr(), shape[1], 1 if rotate is None or rotate[i] else 0
-        e.x_stride[:], e.out_stride[:] = xst[:3], ost[:3]
-    shared = positions.dim() == 2
-    _sized_ptr(positions, torch.int32, (T, plan.n_axes) if shared else (B, T, plan.n_axes), dev, "positions")
-    _check(_lib.lf_rope(ctypes.byref(plan), B, T, _dtype_code(dtype), positions.data_ptr(),
-                        0 if shared else T * plan.n_axes, io, n, 1 if backward else 0, _stream(stream)), "lf_rope")
-
-
-def _norm_vectors(shape: NormGateShape, dev: int, tensors: dict) -> _NormVectors:
+        io += _ROPE_IO(x.data_ptr(), o.data_ptr(), xb, xh, xt, ob, oh, ot, shape[1], 1 if rotate is None or rotate[i] else 0)
     import torch
-    v = _NormVectors()
-    for name, t in tensors.items():
-        if t is not None:
-            want = (shape.groups, shape.dim) if name in ("gate", "scale", "shift") else (shape.dim,)
-            setattr(v, name, _sized_ptr(t, torch.float32, want, dev, name))
-    return v
+    shared = positions.dim() == 2
+    pos = _sized_ptr(positions, torch.int32, (T, plan.n_axes) if shared else (B, T, plan.n_axes), dev, "positions")
+    _check(_lib.lf_rope(ctypes.byref(plan), B, T, _dtype_code(dtype), pos, 0 if shared else T * plan.n_axes, io, n,
+                        1 if backward else 0, _raw_stream(stream, dev)), "lf_rope")
+
+
+_ROPE_IO = struct.Struct("@PP6qii").pack  # an lf_rope_io
+
+
+def _refuse_rope(x, o, dtype, dev) -> None:
+    for t, name in ((x, "x"), (o, "out")):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+        if t.device.index != dev:
+            raise ValueError(f"{name} must be on the current device (cuda:{dev}), got {t.device}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+_NORM_PACK = struct.Struct("@7P").pack  # an lf_norm_gate_vectors
+
+
+def _norm_vectors(shape: NormGateShape, dev: int, gate=None, scale=None, shift=None, pre_w=None, pre_b=None, post_w=None,
+                  post_b=None) -> bytes:
+    import torch
+    f32, group, row = torch.float32, (shape.groups, shape.dim), (shape.dim,)
+    return _NORM_PACK(
+        0 if gate is None else _sized_ptr(gate, f32, group, dev, "gate"),
+        0 if scale is None else _sized_ptr(scale, f32, group, dev, "scale"),
+        0 if shift is None else _sized_ptr(shift, f32, group, dev, "shift"),
+        0 if pre_w is None else _sized_ptr(pre_w, f32, row, dev, "pre_w"),
+        0 if pre_b is None else _sized_ptr(pre_b, f32, row, dev, "pre_b"),
+        0 if post_w is None else _sized_ptr(post_w, f32, row, dev, "post_w"),
+        0 if post_b is None else _sized_ptr(post_b, f32, row, dev, "post_b"))
 
 
 def _norm_dtypes(shape: NormGateShape):
@@ -599,10 +630,9 @@ def lf_norm_gate(shape: NormGateShape, x, y, r, h, gate=None, scale=None, shift=
     def opt(t, dtype, name):
         return None if t is None else _sized_ptr(t, dtype, want, dev, name)
 
-    v = _norm_vectors(shape, dev, dict(gate=gate, scale=scale, shift=shift, pre_w=pre_w, pre_b=pre_b, post_w=post_w,
-                                       post_b=post_b))
-    _check(_lib.lf_norm_gate(ctypes.byref(shape), ctypes.byref(v), _sized_ptr(x, xd, want, dev, "x"), opt(y, yd, "y"),
-                             opt(r, xd, "r"), opt(h, yd, "h"), _stream(stream)), "lf_norm_gate")
+    v = _norm_vectors(shape, dev, gate, scale, shift, pre_w, pre_b, post_w, post_b)
+    _check(_lib.lf_norm_gate(ctypes.byref(shape), v, _sized_ptr(x, xd, want, dev, "x"), opt(y, yd, "y"),
+                             opt(r, xd, "r"), opt(h, yd, "h"), _raw_stream(stream, dev)), "lf_norm_gate")
 
 
 def lf_norm_gate_bwd_workspace(shape: NormGateShape) -> int:
@@ -630,13 +660,12 @@ def lf_norm_gate_bwd(shape: NormGateShape, x, y, dr, dh, dx, dy, grads: dict, wo
     for name in grads:
         if name not in _NORM_VECTORS:
             raise ValueError(f"unknown gradient {name}")
-    v = _norm_vectors(shape, dev, dict(gate=gate, scale=scale, shift=shift, pre_w=pre_w, pre_b=pre_b, post_w=post_w,
-                                       post_b=post_b))
-    g = _norm_vectors(shape, dev, grads)
+    v = _norm_vectors(shape, dev, gate, scale, shift, pre_w, pre_b, post_w, post_b)
+    g = _norm_vectors(shape, dev, **grads)
     _check(_lib.lf_norm_gate_bwd(
-        ctypes.byref(shape), ctypes.byref(v), _sized_ptr(x, xd, want, dev, "x"), opt(y, yd, "y"), opt(dr, xd, "dr"),
-        opt(dh, yd, "dh"), opt(dx, xd, "dx"), opt(dy, yd, "dy"), ctypes.byref(g),
-        _sized_ptr(workspace, torch.uint8, workspace.shape, dev, "workspace"), workspace.numel(), _stream(stream)),
+        ctypes.byref(shape), v, _sized_ptr(x, xd, want, dev, "x"), opt(y, yd, "y"), opt(dr, xd, "dr"),
+        opt(dh, yd, "dh"), opt(dx, xd, "dx"), opt(dy, yd, "dy"), g,
+        _sized_ptr(workspace, torch.uint8, workspace.shape, dev, "workspace"), workspace.numel(), _raw_stream(stream, dev)),
         "lf_norm_gate_bwd")
 
 

@@ -847,7 +847,7 @@ lf_status lf_norm_gate(const lf_norm_gate_shape* shape, const lf_norm_gate_vecto
                        const void* y, void* r, void* h, void* stream)
 {
     const bool empty = shape && shape->rows == 0;  // nothing is there, so null pointers say nothing
-    const lf_status st = check_norm(shape, vectors, empty || y, !empty && h);
+    lf_status st = check_norm(shape, vectors, empty || y, !empty && h);
     if (st != LF_OK) return st;
     if (empty) return LF_OK;
     if (!r && !h) return LF_ERR_NULL;
@@ -858,6 +858,7 @@ lf_status lf_norm_gate(const lf_norm_gate_shape* shape, const lf_norm_gate_vecto
     a.y = y;
     a.r = r;
     a.h = h;
+    if ((st = error_word(&a.err)) != LF_OK) return st;
     return launch_status(lf::launch_norm_fwd(a, shape->x_dtype, shape->y_dtype, static_cast<cudaStream_t>(stream)));
 }
 
@@ -865,7 +866,7 @@ int64_t lf_norm_gate_bwd_workspace(const lf_norm_gate_shape* shape)
 {
     if (check_norm(shape, nullptr, true, false) != LF_OK) return -1;
     const int64_t per = norm_group_rows(shape), groups = (shape->rows + per - 1) / per;
-    return (lf::norm_bwd_ctas(shape->rows) + groups) * 4 * ((shape->dim + 7) / 8 * 8) * 4;
+    return (2 * lf::norm_bwd_ctas(shape->rows) + groups) * 4 * ((shape->dim + 7) / 8 * 8) * 4;
 }
 
 lf_status lf_norm_gate_bwd(const lf_norm_gate_shape* shape, const lf_norm_gate_vectors* vectors, const void* x,
@@ -906,8 +907,11 @@ lf_status lf_norm_gate_bwd(const lf_norm_gate_shape* shape, const lf_norm_gate_v
     a.dh = dh;
     a.dx = dx;
     a.dy = dy;
-    a.part = static_cast<float*>(workspace);
+    if ((st = error_word(&a.err)) != LF_OK) return st;
     a.n_cta = lf::norm_bwd_ctas(shape->rows);
+    a.part_w = static_cast<float*>(workspace);
+    a.part = a.part_w + static_cast<long long>(a.n_cta) * 4 * ((shape->dim + 7) / 8 * 8);
+    a.weights = a.dpre_w || a.dpre_b || a.dpost_w || a.dpost_b;
     a.rows_per_cta = (shape->rows + a.n_cta - 1) / a.n_cta;
     a.n_cta = static_cast<int>((shape->rows + a.rows_per_cta - 1) / a.rows_per_cta);
     return launch_status(lf::launch_norm_bwd(a, shape->x_dtype, shape->y_dtype, static_cast<cudaStream_t>(stream)));

@@ -23,12 +23,22 @@
 // mean, never as a difference of squares. Sums and statistics are fp32; the only
 // roundings to fewer bits are the stores of r, h, dx and dy.
 //
-// The gradient kernel keeps its column sums in registers: a CTA takes consecutive rows,
-// writes one partial row per group it meets (slot = CTA + group, so no two coincide), and
-// a second kernel adds them up in a fixed order -- no atomics, the same bits every time.
+// CTAs are persistent and take consecutive rows, so the vectors of a group stay in
+// registers, folded to what a row needs (gate w2, gate b2, (1 + scale) w1, b1 (1 + scale) +
+// shift), and rows arrive ahead through a ring of bulk copies: a row has several dependent
+// sums, and only loads that are many rows ahead keep the memory busy meanwhile. Rows that do
+// not start on 16-byte boundaries (dim not a multiple of 8), and rows too long for a ring,
+// are loaded directly.
+//
+// The gradient kernel keeps its column sums in registers: a CTA writes one partial row per
+// group it meets (slot = CTA + group, so no two coincide) and one of its weights' sums, and a
+// second kernel adds them up in a fixed order -- no atomics, the same bits every time.
 #include "lf_norm.h"
 #include "lf_device.cuh"
 #include "lf_types.cuh"
+
+#include <algorithm>
+#include <atomic>
 
 namespace lf {
 namespace {
@@ -91,22 +101,30 @@ __device__ __forceinline__ void store8(T* row, int col, int dim, bool al, const 
     }
 }
 
-// A vector parameter's eight values (`other` where it is absent, zeros past dim).
+// Eight values of a vector (`other` where it is absent, zeros past dim).
 __device__ __forceinline__ void load_param(const float* p, int col, int dim, bool al, float other, float (&v)[8])
 {
     if (!p) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = other;
+        for (int i = 0; i < 8; ++i) v[i] = col + i < dim ? other : 0.f;
     } else {
         unpack8(load_raw(p, col, dim, al), v);
     }
 }
 
-// Row sums over a team of `threads` threads (whole warps): two values at once, in a fixed
-// order. Consecutive calls alternate between two buffers, so one barrier a call is enough.
+constexpr int MAX_TEAMS = 8, MAX_STAGES = 4;
+
+// Row sums over a team of whole warps: two values at once, in a fixed order. Consecutive calls
+// alternate between two buffers, so one barrier a call is enough.
 struct Team {
     float (*red)[2][32];  // [2 buffers][2 values][warps of the CTA]
     int warp0, warps, warp, lane, bar, threads, phase;
+
+    __device__ __forceinline__ void sync()
+    {
+        if (warps == 1) __syncwarp();
+        else named_bar_sync(bar, threads);
+    }
 
     __device__ __forceinline__ void sum(float& p, float& q)
     {
@@ -126,6 +144,18 @@ struct Team {
             p += red[phase][0][warp0 + w];
             q += red[phase][1][warp0 + w];
         }
+        phase ^= 1;
+    }
+
+    __device__ __forceinline__ void sum(float& p)
+    {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) p += __shfl_xor_sync(0xffffffffu, p, o);
+        if (warps == 1) return;
+        if (lane == 0) red[phase][0][warp] = p;
+        named_bar_sync(bar, threads);
+        p = 0.f;
+        for (int w = 0; w < warps; ++w) p += red[phase][0][warp0 + w];
         phase ^= 1;
     }
 };
@@ -151,14 +181,13 @@ template <int NV>
 __device__ __forceinline__ float normalise(Team& team, float (&t)[NV][8], int kind, int dim, int col0, int stride, float eps)
 {
     const float inv = 1.0f / static_cast<float>(dim);
-    float unused = 0.f;
     if (kind == NORM_LAYER) {
         float s = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
             for (int i = 0; i < 8; ++i) s += t[k][i];
-        team.sum(s, unused);
+        team.sum(s);
         const float mean = s * inv;
 #pragma unroll
         for (int k = 0; k < NV; ++k)
@@ -170,7 +199,7 @@ __device__ __forceinline__ float normalise(Team& team, float (&t)[NV][8], int ki
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int i = 0; i < 8; ++i) q = fmaf(t[k][i], t[k][i], q);
-    team.sum(q, unused);
+    team.sum(q);
     const float rs = 1.0f / sqrtf(q * inv + eps);
 #pragma unroll
     for (int k = 0; k < NV; ++k)
@@ -179,88 +208,222 @@ __device__ __forceinline__ float normalise(Team& team, float (&t)[NV][8], int ki
     return rs;
 }
 
-constexpr int NORM_THREADS = 512;
+// One untiled bulk copy, issued by one thread.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// A team's rows, arriving through a ring of `stages` rows of N streams in shared memory (or
+// loaded directly when stages == 0). Stream n of a row has esize[n] bytes an element; a null
+// stream is skipped. Rows are first, first + step, ... below end.
+template <int N>
+struct Rows {
+    const uint8_t* src[N];
+    uint32_t bytes[N], at[N];  // bytes of a row, offset in a stage
+    uint32_t stage_bytes;
+    uint8_t* ring;
+    uint64_t* full;
+    int stages, used;
+    long long step, end;
+    bool leader;
+
+    __device__ __forceinline__ void issue(long long row, int s)
+    {
+        uint32_t sum = 0;
+#pragma unroll
+        for (int n = 0; n < N; ++n) sum += src[n] ? bytes[n] : 0u;
+        mbar_arrive_expect_tx(&full[s], sum);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            if (src[n]) bulk_load(ring + s * stage_bytes + at[n], src[n] + row * bytes[n], bytes[n], &full[s]);
+    }
+
+    __device__ __forceinline__ void start(long long first)
+    {
+        used = 0;
+        if (leader)
+            for (int s = 0; s < stages; ++s)
+                if (first + s * step < end) issue(first + s * step, s);
+    }
+
+    // Waits for the next row; its stage's address.
+    __device__ __forceinline__ const uint8_t* wait(volatile int* abort_flag, int* err, bool* ok)
+    {
+        const int s = used % stages;
+        *ok = mbar_wait(&full[s], (used / stages) & 1, abort_flag, err, 0x70);
+        return ring + s * stage_bytes;
+    }
+
+    // The whole team has read `row`'s stage: its next use is filled.
+    __device__ __forceinline__ void release(long long row)
+    {
+        if (leader && row + stages * step < end) issue(row + stages * step, used % stages);
+        ++used;
+    }
+
+    // After an expired wait: every copy issued lands before the CTA leaves.
+    __device__ __forceinline__ void drain()
+    {
+        if (leader)
+            for (int s = 0; s < stages; ++s)
+                for (int p = 0; p < 2; ++p) mbar_drain(&full[s], p, 10000000ull);
+    }
+};
+
+template <int N>
+__device__ __forceinline__ Rows<N> make_rows(const void* const (&src)[N], const int (&esize)[N], int dim, uint8_t* smem,
+                                             uint64_t* full, int stages, int team, int team_thread, int teams, long long end)
+{
+    Rows<N> r;
+    uint32_t at = 0;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        r.src[n] = static_cast<const uint8_t*>(src[n]);
+        r.bytes[n] = static_cast<uint32_t>(dim) * esize[n];
+        r.at[n] = at;
+        at += src[n] ? r.bytes[n] : 0u;
+    }
+    r.stage_bytes = at;
+    r.ring = smem + static_cast<size_t>(team) * stages * at;
+    r.full = full + team * MAX_STAGES;
+    r.stages = stages;
+    r.step = teams;
+    r.end = end;
+    r.leader = team_thread == 0;
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> stage_raw(const uint8_t* stage, uint32_t at, int col, int dim)
+{
+    return load_raw(reinterpret_cast<const T*>(stage + at), col, dim, true);
+}
+
+// A CTA has up to 256 threads where a thread holds one group of eight, 512 where it holds more.
+// Registers a thread: what lets NORM_FWD_CTAS_PER_SM and NORM_BWD_CTAS_PER_SM CTAs of 192 threads
+// (1536 columns) share an SM; all there are where one CTA has the SM to itself.
+template <int NV> constexpr int FWD_REGS = NV == 1 ? 80 : 128;
+template <int NV> constexpr int BWD_REGS = NV == 1 ? 112 : 128;
 
 template <typename TX, typename TY, int NV>
-__global__ void __launch_bounds__(NORM_THREADS) norm_fwd_kernel(const NormArgs a, int team_threads, bool al)
+__global__ void __maxnreg__(FWD_REGS<NV>) norm_fwd_kernel(const NormArgs a, int team_threads, int stages, bool al)
 {
     __shared__ float red[2][2][32];
+    __shared__ uint64_t full[MAX_TEAMS * MAX_STAGES];
+    __shared__ int abort_word;
+    extern __shared__ __align__(16) uint8_t smem[];
     Team team = make_team(red, team_threads);
     const int teams = blockDim.x / team_threads;
     const int ti = threadIdx.x / team_threads, tt = threadIdx.x - ti * team_threads;
-    const long long row = static_cast<long long>(blockIdx.x) * teams + ti;
-    if (row >= a.rows) return;  // whole teams leave
-    const int col0 = tt * 8, stride = team_threads * 8;
-    const long long at = row * a.dim;
-    Raw8<TX> xr[NV];
-    Raw8<TY> yr[NV];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        xr[k] = load_raw(static_cast<const TX*>(a.x) + at, col0 + k * stride, a.dim, al);
-        if (a.y) yr[k] = load_raw(static_cast<const TY*>(a.y) + at, col0 + k * stride, a.dim, al);
+    const int col0 = tt * 8, stride = team_threads * 8, dim = a.dim;
+    const long long r0 = blockIdx.x * a.rows_per_cta;
+    const long long r1 = min(a.rows, r0 + a.rows_per_cta);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < teams * MAX_STAGES; ++i) mbar_init(&full[i], 1);
+        abort_word = 0;
+        fence_mbar_init();
     }
-    const long long g = (row / a.per_group) * a.dim;
-    float t[NV][8];
-    if (a.y) {
-#pragma unroll
-        for (int k = 0; k < NV; ++k) unpack8(yr[k], t[k]);
-        if (a.post != NORM_NONE) normalise<NV>(team, t, a.post, a.dim, col0, stride, a.eps);
-    }
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int col = col0 + k * stride;
-        float x[8], p[8];
-        unpack8(xr[k], x);
-        if (a.y) {
-            if (a.v.post_w) {
-                load_param(a.v.post_w, col, a.dim, al, 1.f, p);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) t[k][i] *= p[i];
+    __syncthreads();
+    volatile int* abort_flag = &abort_word;
+    const void* src[2] = {a.x, a.y};
+    const int esize[2] = {sizeof(TX), sizeof(TY)};
+    Rows<2> in = make_rows<2>(src, esize, dim, smem, full, stages, ti, tt, teams, r1);
+    in.start(r0 + ti);
+
+    long long group = -1;
+    float g2[NV][8], b2[NV][8], s1[NV][8], t1[NV][8];  // r = alpha x + m g2 + b2, h = n s1 + t1
+    for (long long row = r0 + ti; row < r1; row += teams) {
+        Raw8<TX> xr[NV];
+        Raw8<TY> yr[NV];
+        if (stages) {
+            bool ok;
+            const uint8_t* st = in.wait(abort_flag, a.err, &ok);
+            if (!ok) {
+                in.drain();
+                return;  // the whole team: it waits on one barrier
             }
-            if (a.v.post_b) {
-                load_param(a.v.post_b, col, a.dim, al, 0.f, p);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) t[k][i] += p[i];
+            for (int k = 0; k < NV; ++k) {
+                xr[k] = stage_raw<TX>(st, in.at[0], col0 + k * stride, dim);
+                if (a.y) yr[k] = stage_raw<TY>(st, in.at[1], col0 + k * stride, dim);
             }
-            load_param(a.v.gate ? a.v.gate + g : nullptr, col, a.dim, al, 1.f, p);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) t[k][i] = fmaf(p[i], t[k][i], a.alpha * x[i]);
+            team.sync();
+            in.release(row);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t[k][i] = a.alpha * x[i];
+            for (int k = 0; k < NV; ++k) {
+                xr[k] = load_raw(static_cast<const TX*>(a.x) + row * dim, col0 + k * stride, dim, al);
+                if (a.y) yr[k] = load_raw(static_cast<const TY*>(a.y) + row * dim, col0 + k * stride, dim, al);
+            }
         }
-        if (a.r) store8(static_cast<TX*>(a.r) + at, col, a.dim, al, t[k]);
-    }
-    if (!a.h) return;
-    normalise<NV>(team, t, a.pre, a.dim, col0, stride, a.eps);
+        if (row / a.per_group != group) {
+            group = row / a.per_group;
+            const long long g = group * dim;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int col = col0 + k * stride;
-        float p[8], q[8];
-        if (a.v.pre_w) {
-            load_param(a.v.pre_w, col, a.dim, al, 1.f, p);
+            for (int k = 0; k < NV; ++k) {
+                const int col = col0 + k * stride;
+                float p[8];
+                load_param(a.v.gate ? a.v.gate + g : nullptr, col, dim, al, 1.f, p);
+                load_param(a.v.post_w, col, dim, al, 1.f, g2[k]);
+                load_param(a.v.post_b, col, dim, al, 0.f, b2[k]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t[k][i] *= p[i];
+                for (int i = 0; i < 8; ++i) {
+                    g2[k][i] *= p[i];
+                    b2[k][i] *= p[i];
+                }
+                load_param(a.v.scale ? a.v.scale + g : nullptr, col, dim, al, 0.f, p);
+                load_param(a.v.pre_w, col, dim, al, 1.f, s1[k]);
+                load_param(a.v.pre_b, col, dim, al, 0.f, t1[k]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    s1[k][i] *= 1.f + p[i];
+                    t1[k][i] *= 1.f + p[i];
+                }
+                load_param(a.v.shift ? a.v.shift + g : nullptr, col, dim, al, 0.f, p);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) t1[k][i] += p[i];
+            }
         }
-        if (a.v.pre_b) {
-            load_param(a.v.pre_b, col, a.dim, al, 0.f, p);
+        float t[NV][8];
+        if (a.y) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t[k][i] += p[i];
+            for (int k = 0; k < NV; ++k) unpack8(yr[k], t[k]);
+            if (a.post != NORM_NONE) normalise<NV>(team, t, a.post, dim, col0, stride, a.eps);
         }
-        load_param(a.v.scale ? a.v.scale + g : nullptr, col, a.dim, al, 0.f, p);
-        load_param(a.v.shift ? a.v.shift + g : nullptr, col, a.dim, al, 0.f, q);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[k][i] = fmaf(t[k][i], 1.f + p[i], q[i]);
-        store8(static_cast<TY*>(a.h) + at, col, a.dim, al, t[k]);
+        for (int k = 0; k < NV; ++k) {
+            float x[8];
+            unpack8(xr[k], x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[i] *= a.alpha;
+                t[k][i] = a.y ? fmaf(g2[k][i], t[k][i], x[i] + b2[k][i]) : x[i];
+            }
+            if (a.r) store8(static_cast<TX*>(a.r) + row * dim, col0 + k * stride, dim, al, t[k]);
+        }
+        if (!a.h) continue;
+        normalise<NV>(team, t, a.pre, dim, col0, stride, a.eps);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[k][i] = fmaf(t[k][i], s1[k][i], t1[k][i]);
+            store8(static_cast<TY*>(a.h) + row * dim, col0 + k * stride, dim, al, t[k]);
+        }
     }
 }
 
-// Values past dim are kept at zero wherever they enter a sum.
+// A[j] of the header, and how many of the four are kept: A3 (sum dr') only where the post
+// norm has a bias or its gradient is wanted.
 template <typename TX, typename TY, int NV>
-__global__ void __launch_bounds__(NORM_THREADS) norm_bwd_kernel(const NormArgs a, int team_threads, bool al)
+__global__ void __maxnreg__(BWD_REGS<NV>) norm_bwd_kernel(const NormArgs a, int team_threads, int stages, bool al)
 {
     __shared__ float red[2][2][32];
-    extern __shared__ float fold[];  // [teams - 1][dim8] while the teams' sums are added
+    __shared__ uint64_t full[MAX_TEAMS * MAX_STAGES];
+    __shared__ int abort_word;
+    extern __shared__ __align__(16) uint8_t smem[];  // the rings, then [teams - 1][dim8] floats
     Team team = make_team(red, team_threads);
     const int teams = blockDim.x / team_threads;
     const int ti = threadIdx.x / team_threads, tt = threadIdx.x - ti * team_threads;
@@ -269,11 +432,44 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_kernel(const NormArgs a
     const long long r0 = blockIdx.x * a.rows_per_cta;
     const long long r1 = min(a.rows, r0 + a.rows_per_cta);
     const float inv = 1.0f / static_cast<float>(dim);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < teams * MAX_STAGES; ++i) mbar_init(&full[i], 1);
+        abort_word = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    volatile int* abort_flag = &abort_word;
+    const void* src[4] = {a.x, a.y, a.dr, a.dh};
+    const int esize[4] = {sizeof(TX), sizeof(TY), sizeof(TX), sizeof(TY)};
+    Rows<4> in = make_rows<4>(src, esize, dim, smem, full, stages, ti, tt, teams, r1);
+    in.start(r0 + ti);
+    float* fold = reinterpret_cast<float*>(smem + static_cast<size_t>(teams) * stages * in.stage_bytes);
+    float* part_w = a.part_w + static_cast<long long>(blockIdx.x) * 4 * dim8;
 
+    long long row = r0 + ti;
+    bool broken = false;
     for (long long seg = r0; seg < r1;) {
         const long long gi = seg / a.per_group;
         const long long seg_end = min(r1, (gi + 1) * a.per_group);
         const long long g = gi * dim;
+        float g2[NV][8], b2[NV][8], s1[NV][8];  // u gate = m g2 + b2; dn = dh s1
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int col = col0 + k * stride;
+            float p[8];
+            load_param(a.v.gate ? a.v.gate + g : nullptr, col, dim, al, 1.f, p);
+            load_param(a.v.post_w, col, dim, al, 1.f, g2[k]);
+            load_param(a.v.post_b, col, dim, al, 0.f, b2[k]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                g2[k][i] *= p[i];
+                b2[k][i] *= p[i];
+            }
+            load_param(a.v.scale ? a.v.scale + g : nullptr, col, dim, al, 0.f, p);
+            load_param(a.v.pre_w, col, dim, al, 1.f, s1[k]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s1[k][i] *= 1.f + p[i];
+        }
         float A[4][NV][8];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -281,70 +477,69 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_kernel(const NormArgs a
             for (int k = 0; k < NV; ++k)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) A[j][k][i] = 0.f;
-        for (long long row = seg + ti; row < seg_end; row += teams) {
+        for (; row < seg_end && !broken; row += teams) {
             const long long at = row * dim;
-            float m[NV][8], n[NV][8], d[NV][8], p[8];
+            const TX *x_row = static_cast<const TX*>(a.x) + at, *dr_row = static_cast<const TX*>(a.dr) + at;
+            const TY *y_row = static_cast<const TY*>(a.y) + at, *dh_row = static_cast<const TY*>(a.dh) + at;
+            if (stages) {
+                bool ok;
+                const uint8_t* st = in.wait(abort_flag, a.err, &ok);
+                if (!ok) {
+                    in.drain();
+                    broken = true;
+                    break;
+                }
+                x_row = reinterpret_cast<const TX*>(st + in.at[0]);
+                y_row = reinterpret_cast<const TY*>(st + in.at[1]);
+                dr_row = reinterpret_cast<const TX*>(st + in.at[2]);
+                dh_row = reinterpret_cast<const TY*>(st + in.at[3]);
+            }
+            float m[NV][8], n[NV][8], d[NV][8];
             float rs1 = 1.f, rs2 = 1.f;
             // forward again: m = post(y), n = pre(r)
+            if (a.y) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                if (a.y) unpack8(load_raw(static_cast<const TY*>(a.y) + at, col0 + k * stride, dim, al), m[k]);
-                unpack8(load_raw(static_cast<const TX*>(a.x) + at, col0 + k * stride, dim, al), n[k]);
+                for (int k = 0; k < NV; ++k) unpack8(load_raw(y_row, col0 + k * stride, dim, al), m[k]);
+                if (a.post != NORM_NONE) rs2 = normalise<NV>(team, m, a.post, dim, col0, stride, a.eps);
             }
-            if (a.y && a.post != NORM_NONE) rs2 = normalise<NV>(team, m, a.post, dim, col0, stride, a.eps);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int col = col0 + k * stride;
+                unpack8(load_raw(x_row, col0 + k * stride, dim, al), n[k]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) n[k][i] *= a.alpha;
-                if (a.y) {
-                    float u[8];
-                    load_param(a.v.post_w, col, dim, al, 1.f, p);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) u[i] = m[k][i] * p[i];
-                    load_param(a.v.post_b, col, dim, al, 0.f, p);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) u[i] += p[i];
-                    load_param(a.v.gate ? a.v.gate + g : nullptr, col, dim, al, 1.f, p);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) n[k][i] = fmaf(p[i], u[i], n[k][i]);
+                for (int i = 0; i < 8; ++i) {
+                    n[k][i] *= a.alpha;
+                    if (a.y) n[k][i] = fmaf(g2[k][i], m[k][i], n[k][i] + b2[k][i]);
                 }
             }
-            float s1 = 0.f, s2 = 0.f;
+            float q1 = 0.f, q2 = 0.f;
             if (a.dh) {
                 rs1 = normalise<NV>(team, n, a.pre, dim, col0, stride, a.eps);
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
-                    const int col = col0 + k * stride;
-                    unpack8(load_raw(static_cast<const TY*>(a.dh) + at, col, dim, al), d[k]);
+                    unpack8(load_raw(dh_row, col0 + k * stride, dim, al), d[k]);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         A[0][k][i] += d[k][i];
                         A[1][k][i] = fmaf(d[k][i], n[k][i], A[1][k][i]);
-                    }
-                    load_param(a.v.scale ? a.v.scale + g : nullptr, col, dim, al, 0.f, p);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) d[k][i] *= 1.f + p[i];
-                    load_param(a.v.pre_w, col, dim, al, 1.f, p);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        d[k][i] *= p[i];
-                        s1 += d[k][i];
-                        s2 = fmaf(d[k][i], n[k][i], s2);
+                        d[k][i] *= s1[k][i];
+                        q1 += d[k][i];
+                        q2 = fmaf(d[k][i], n[k][i], q2);
                     }
                 }
-                team.sum(s1, s2);
-                s1 = a.pre == NORM_LAYER ? s1 * inv : 0.f;
-                s2 *= inv;
+                team.sum(q1, q2);
+                q1 = a.pre == NORM_LAYER ? q1 * inv : 0.f;
+                q2 *= inv;
             }
             // dr' in d
+            float p1 = 0.f, p2 = 0.f;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int col = col0 + k * stride;
-                if (a.dr) unpack8(load_raw(static_cast<const TX*>(a.dr) + at, col, dim, al), p);
+                float p[8];
+                if (a.dr) unpack8(load_raw(dr_row, col, dim, al), p);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float dn = a.dh ? rs1 * (d[k][i] - s1 - n[k][i] * s2) : 0.f;
+                    const float dn = a.dh ? rs1 * (d[k][i] - q1 - n[k][i] * q2) : 0.f;
                     d[k][i] = (a.dr ? p[i] : 0.f) + dn;
                 }
                 if (a.dx) {
@@ -352,42 +547,36 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_kernel(const NormArgs a
                     for (int i = 0; i < 8; ++i) p[i] = a.alpha * d[k][i];
                     store8(static_cast<TX*>(a.dx) + at, col, dim, al, p);
                 }
+                if (a.y) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        A[2][k][i] += d[k][i];
+                        A[3][k][i] = fmaf(d[k][i], m[k][i], A[3][k][i]);
+                        d[k][i] *= g2[k][i];  // dm (zero past dim, as g2 is)
+                        p1 += d[k][i];
+                        p2 = fmaf(d[k][i], m[k][i], p2);
+                    }
+                }
             }
-            if (!a.y) continue;
-            float t1 = 0.f, t2 = 0.f;
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int col = col0 + k * stride;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    A[2][k][i] += d[k][i];
-                    A[3][k][i] = fmaf(d[k][i], m[k][i], A[3][k][i]);
-                }
-                load_param(a.v.gate ? a.v.gate + g : nullptr, col, dim, al, 1.f, p);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) d[k][i] *= p[i];
-                load_param(a.v.post_w, col, dim, al, 1.f, p);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    d[k][i] = col + i < dim ? d[k][i] * p[i] : 0.f;
-                    t1 += d[k][i];
-                    t2 = fmaf(d[k][i], m[k][i], t2);
-                }
+            if (stages) {
+                team.sync();
+                in.release(row);
             }
             if (!a.dy) continue;
             if (a.post != NORM_NONE) {
-                team.sum(t1, t2);
-                t1 = a.post == NORM_LAYER ? t1 * inv : 0.f;
-                t2 *= inv;
+                team.sum(p1, p2);
+                p1 = a.post == NORM_LAYER ? p1 * inv : 0.f;
+                p2 *= inv;
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) d[k][i] = rs2 * (d[k][i] - t1 - m[k][i] * t2);
+                    for (int i = 0; i < 8; ++i) d[k][i] = rs2 * (d[k][i] - p1 - m[k][i] * p2);
             }
 #pragma unroll
             for (int k = 0; k < NV; ++k) store8(static_cast<TY*>(a.dy) + at, col0 + k * stride, dim, al, d[k]);
         }
-        // the CTA's sums for this group: teams added in order, one partial row each
+        // the CTA's sums for this group: teams added in order, one partial row each; and the
+        // weights' sums so far
         float* slot = a.part + (blockIdx.x + gi) * 4 * dim8;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -398,9 +587,9 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_kernel(const NormArgs a
                     for (int k = 0; k < NV; ++k) {
                         const int col = col0 + k * stride;
                         if (col < dim8) {
-                            float* f = fold + (ti - 1) * dim8 + col;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) f[i] = A[j][k][i];
+                            float4* f = reinterpret_cast<float4*>(fold + (ti - 1) * dim8 + col);
+                            f[0] = make_float4(A[j][k][0], A[j][k][1], A[j][k][2], A[j][k][3]);
+                            f[1] = make_float4(A[j][k][4], A[j][k][5], A[j][k][6], A[j][k][7]);
                         }
                     }
                 }
@@ -414,8 +603,25 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_kernel(const NormArgs a
                         for (int o = 0; o < teams - 1; ++o)
 #pragma unroll
                             for (int i = 0; i < 8; ++i) A[j][k][i] += fold[o * dim8 + col + i];
-                        *reinterpret_cast<float4*>(slot + j * dim8 + col) = make_float4(A[j][k][0], A[j][k][1], A[j][k][2], A[j][k][3]);
-                        *reinterpret_cast<float4*>(slot + j * dim8 + col + 4) = make_float4(A[j][k][4], A[j][k][5], A[j][k][6], A[j][k][7]);
+                        float4* to = reinterpret_cast<float4*>(slot + j * dim8 + col);
+                        to[0] = make_float4(A[j][k][0], A[j][k][1], A[j][k][2], A[j][k][3]);
+                        to[1] = make_float4(A[j][k][4], A[j][k][5], A[j][k][6], A[j][k][7]);
+                        if (a.weights) {  // times 1 + scale, or the gate
+                            const float* f = j < 2 ? a.v.scale : a.v.gate;
+                            float p[8];
+                            load_param(f ? f + g : nullptr, col, dim, al, j < 2 ? 0.f : 1.f, p);
+                            float4* w = reinterpret_cast<float4*>(part_w + j * dim8 + col);
+                            float o[8] = {};
+                            if (seg > r0) {
+                                const float4 lo = w[0], hi = w[1];
+                                o[0] = lo.x; o[1] = lo.y; o[2] = lo.z; o[3] = lo.w;
+                                o[4] = hi.x; o[5] = hi.y; o[6] = hi.z; o[7] = hi.w;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o[i] = fmaf(j < 2 ? 1.f + p[i] : p[i], A[j][k][i], o[i]);
+                            w[0] = make_float4(o[0], o[1], o[2], o[3]);
+                            w[1] = make_float4(o[4], o[5], o[6], o[7]);
+                        }
                     }
                 }
             }
@@ -424,54 +630,48 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_kernel(const NormArgs a
     }
 }
 
-constexpr int FIN_COLS = 32, FIN_ROWS = 16;
+constexpr int FIN_COLS = 32, FIN_ROWS = 32;
 
 // Adds the partial rows up: blockIdx.y < groups is a group's dgate, dscale and dshift, the
-// last one the weights' gradients over all groups. A CTA takes 32 columns, 16 threads each.
+// last one the weights' gradients over all CTAs. A CTA takes 32 columns, 32 threads each.
 __global__ void __launch_bounds__(FIN_COLS * FIN_ROWS) norm_bwd_finish_kernel(const NormArgs a, long long groups)
 {
-    __shared__ float red[FIN_ROWS][4][FIN_COLS];
+    __shared__ float red[4][FIN_ROWS][FIN_COLS];
     const int c = threadIdx.x % FIN_COLS, j = threadIdx.x / FIN_COLS;
     const int col = blockIdx.x * FIN_COLS + c;
     const int dim8 = (a.dim + 7) & ~7;
-    const bool weights = a.dpre_w || a.dpre_b || a.dpost_w || a.dpost_b;
-    for (long long item = blockIdx.y; item < groups + (weights ? 1 : 0); item += gridDim.y) {
+    for (long long item = blockIdx.y; item < groups + (a.weights ? 1 : 0); item += gridDim.y) {
         const bool all = item == groups;
+        // consecutive partial rows: a group's are those of the CTAs that met it
         const long long row0 = all ? 0 : item * a.per_group;
         const long long row1 = all ? a.rows : min(a.rows, row0 + a.per_group);
+        const long long c0 = row0 / a.rows_per_cta;
+        const int n = static_cast<int>((row1 - 1) / a.rows_per_cta - c0) + 1;
+        const float* base = (all ? a.part_w : a.part + (c0 + item) * 4 * dim8) + col;
         float A[4] = {0.f, 0.f, 0.f, 0.f};
-        if (col < a.dim && row1 > row0) {
-            const long long c0 = row0 / a.rows_per_cta, c1 = (row1 - 1) / a.rows_per_cta;
-            for (long long cta = c0 + j; cta <= c1; cta += FIN_ROWS) {
-                // the groups this CTA met, of those wanted
-                const long long first = cta * a.rows_per_cta, last = min(a.rows, first + a.rows_per_cta) - 1;
-                const long long g0 = all ? first / a.per_group : item, g1 = all ? last / a.per_group : item;
-                for (long long g = g0; g <= g1; ++g) {
-                    const float* p = a.part + (cta + g) * 4 * dim8 + col;
-                    float w1 = 1.f, w2 = 1.f;
-                    if (all) {
-                        w1 = a.v.scale ? 1.f + a.v.scale[g * a.dim + col] : 1.f;
-                        w2 = a.v.gate ? a.v.gate[g * a.dim + col] : 1.f;
-                    }
-                    A[0] = fmaf(w1, p[0], A[0]);
-                    A[1] = fmaf(w1, p[dim8], A[1]);
-                    A[2] = fmaf(w2, p[2 * dim8], A[2]);
-                    A[3] = fmaf(w2, p[3 * dim8], A[3]);
-                }
+        if (col < a.dim) {
+#pragma unroll 4
+            for (int s = j; s < n; s += FIN_ROWS) {
+                const float* p = base + static_cast<long long>(s) * 4 * dim8;
+                A[0] += p[0];
+                A[1] += p[dim8];
+                A[2] += p[2 * dim8];
+                A[3] += p[3 * dim8];
             }
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) red[j][i][c] = A[i];
+        for (int i = 0; i < 4; ++i) red[i][j][c] = A[i];
         __syncthreads();
-        if (j < 4 && col < a.dim) {  // thread row i adds sum i
+        if (j < 4) {  // thread row j adds sum j
             float s = 0.f;
-            for (int o = 0; o < FIN_ROWS; ++o) s += red[o][j][c];
-            red[0][j][c] = s;
+#pragma unroll
+            for (int o = 0; o < FIN_ROWS; ++o) s += red[j][o][c];
+            red[j][0][c] = s;
         }
         __syncthreads();
         if (j == 0 && col < a.dim) {
-            const float a1 = red[0][0][c], a2 = red[0][1][c], a3 = red[0][2][c], a4 = red[0][3][c];
+            const float a1 = red[0][0][c], a2 = red[1][0][c], a3 = red[2][0][c], a4 = red[3][0][c];
             if (all) {
                 if (a.dpre_w) a.dpre_w[col] = a2;
                 if (a.dpre_b) a.dpre_b[col] = a1;
@@ -487,55 +687,70 @@ __global__ void __launch_bounds__(FIN_COLS * FIN_ROWS) norm_bwd_finish_kernel(co
     }
 }
 
-// Threads of a team and groups of 8 a thread: as few elements a thread as 256 threads
-// allow, then two groups, then four (dim <= 16384 = 512 * 4 * 8).
-int team_of(int dim, int* nv)
+// How a call's rows are taken: threads of a team and groups of 8 a thread (as few as 256
+// threads allow, then two, then four: dim <= 16384 = 512 * 4 * 8), teams of a CTA, stages of
+// the ring (as many as leave `ctas` CTAs an SM; fewer than two are not worth a ring).
+struct NormPlan {
+    int nv, threads, teams, stages;
+    size_t smem;
+};
+
+NormPlan plan_of(const NormArgs& a, size_t row_bytes, int ctas, bool fold)
 {
-    const int vecs = (dim + 7) / 8;
-    *nv = vecs <= 256 ? 1 : (vecs <= 1024 ? 2 : 4);
-    const int t = (vecs + *nv - 1) / *nv;
-    return (t + 31) / 32 * 32;
+    NormPlan p;
+    const int vecs = (a.dim + 7) / 8;
+    p.nv = vecs <= 256 ? 1 : (vecs <= 1024 ? 2 : 4);
+    p.threads = ((vecs + p.nv - 1) / p.nv + 31) / 32 * 32;
+    p.teams = p.nv > 1 ? 1 : std::min(MAX_TEAMS, 256 / p.threads);
+    const size_t extra = fold ? static_cast<size_t>(p.teams - 1) * vecs * 8 * sizeof(float) : 0;
+    const size_t room = (220u * 1024u) / ctas - 2048 - extra;
+    const int fit = static_cast<int>(std::min<size_t>(room / (row_bytes * p.teams), MAX_STAGES));
+    p.stages = a.dim % 8 == 0 && fit >= 2 ? fit : 0;
+    p.smem = p.stages * row_bytes * p.teams + extra;
+    return p;
 }
 
-bool aligned_rows(const NormArgs& a) { return a.dim % 8 == 0; }  // pointers are 16-byte aligned
-
-template <typename TX, typename TY>
-cudaError_t launch_fwd(const NormArgs& a, cudaStream_t s)
+// Dynamic shared memory past the default limit (48 KB with the kernel's static part), asked for
+// once a device: the most that a plan uses.
+template <auto KERNEL>
+cudaError_t allow_smem(size_t bytes)
 {
-    int nv;
-    const int t = team_of(a.dim, &nv);
-    const int teams = t >= 256 ? 1 : 256 / t;
-    const unsigned grid = static_cast<unsigned>((a.rows + teams - 1) / teams);
-    const bool al = aligned_rows(a);
-    if (nv == 1)
-        norm_fwd_kernel<TX, TY, 1><<<grid, t * teams, 0, s>>>(a, t, al);
-    else if (nv == 2)
-        norm_fwd_kernel<TX, TY, 2><<<grid, t * teams, 0, s>>>(a, t, al);
-    else
-        norm_fwd_kernel<TX, TY, 4><<<grid, t * teams, 0, s>>>(a, t, al);
+    if (bytes <= 40 * 1024) return cudaSuccess;
+    static std::atomic<bool> set[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64 && set[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) set[dev].store(true, std::memory_order_release);
+    return e;
+}
+
+template <typename TX, typename TY, int NV>
+cudaError_t launch_fwd(NormArgs a, const NormPlan& p, cudaStream_t s)
+{
+    cudaError_t e = allow_smem<norm_fwd_kernel<TX, TY, NV>>(p.smem);
+    if (e != cudaSuccess) return e;
+    // CTAs for all SMs' worth of resident ones; rows are spread evenly over them
+    const long long most = 148ll * (NV == 1 ? NORM_FWD_CTAS_PER_SM : 1);
+    const long long per = std::max<long long>(p.teams, (a.rows + most - 1) / most);
+    a.rows_per_cta = (per + p.teams - 1) / p.teams * p.teams;
+    const unsigned grid = static_cast<unsigned>((a.rows + a.rows_per_cta - 1) / a.rows_per_cta);
+    norm_fwd_kernel<TX, TY, NV><<<grid, p.threads * p.teams, p.smem, s>>>(a, p.threads, p.stages, a.dim % 8 == 0);
     return cudaGetLastError();
 }
 
-template <typename TX, typename TY>
-cudaError_t launch_bwd(const NormArgs& a, cudaStream_t s)
+template <typename TX, typename TY, int NV>
+cudaError_t launch_bwd(const NormArgs& a, const NormPlan& p, cudaStream_t s)
 {
-    int nv;
-    const int t = team_of(a.dim, &nv);
-    const int teams = t >= 256 ? 1 : 256 / t;
-    const bool al = aligned_rows(a);
-    const size_t fold = static_cast<size_t>(teams - 1) * ((a.dim + 7) / 8 * 8) * sizeof(float);
-    if (nv == 1)
-        norm_bwd_kernel<TX, TY, 1><<<a.n_cta, t * teams, fold, s>>>(a, t, al);
-    else if (nv == 2)
-        norm_bwd_kernel<TX, TY, 2><<<a.n_cta, t * teams, fold, s>>>(a, t, al);
-    else
-        norm_bwd_kernel<TX, TY, 4><<<a.n_cta, t * teams, fold, s>>>(a, t, al);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = allow_smem<norm_bwd_kernel<TX, TY, NV>>(p.smem);
     if (e != cudaSuccess) return e;
-    if (!a.dgate && !a.dscale && !a.dshift && !a.dpre_w && !a.dpre_b && !a.dpost_w && !a.dpost_b) return cudaSuccess;
+    norm_bwd_kernel<TX, TY, NV><<<a.n_cta, p.threads * p.teams, p.smem, s>>>(a, p.threads, p.stages, a.dim % 8 == 0);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if (!a.dgate && !a.dscale && !a.dshift && !a.weights) return cudaSuccess;
     const long long groups = (a.rows + a.per_group - 1) / a.per_group;
-    const long long items = groups + 1;
-    norm_bwd_finish_kernel<<<dim3((a.dim + FIN_COLS - 1) / FIN_COLS, static_cast<unsigned>(items < 65535 ? items : 65535)),
+    const long long items = groups + (a.weights ? 1 : 0);
+    norm_bwd_finish_kernel<<<dim3((a.dim + FIN_COLS - 1) / FIN_COLS, static_cast<unsigned>(std::min<long long>(items, 65535))),
                              FIN_COLS * FIN_ROWS, 0, s>>>(a, groups);
     return cudaGetLastError();
 }
@@ -543,8 +758,17 @@ cudaError_t launch_bwd(const NormArgs& a, cudaStream_t s)
 template <bool BWD, typename TX, typename TY>
 cudaError_t launch_one(const NormArgs& a, cudaStream_t s)
 {
-    if constexpr (BWD) return launch_bwd<TX, TY>(a, s);
-    else return launch_fwd<TX, TY>(a, s);
+    const size_t x = static_cast<size_t>(a.dim) * sizeof(TX), y = static_cast<size_t>(a.dim) * sizeof(TY);
+    const size_t row = BWD ? x + (a.y ? y : 0) + (a.dr ? x : 0) + (a.dh ? y : 0) : x + (a.y ? y : 0);
+    const bool small = a.dim <= 2048;
+    const NormPlan p = plan_of(a, row, small ? (BWD ? NORM_BWD_CTAS_PER_SM : NORM_FWD_CTAS_PER_SM) : 1, BWD);
+    if constexpr (BWD) {
+        if (p.nv == 1) return launch_bwd<TX, TY, 1>(a, p, s);
+        return p.nv == 2 ? launch_bwd<TX, TY, 2>(a, p, s) : launch_bwd<TX, TY, 4>(a, p, s);
+    } else {
+        if (p.nv == 1) return launch_fwd<TX, TY, 1>(a, p, s);
+        return p.nv == 2 ? launch_fwd<TX, TY, 2>(a, p, s) : launch_fwd<TX, TY, 4>(a, p, s);
+    }
 }
 
 template <bool BWD>

@@ -10,7 +10,8 @@ namespace lf {
 enum : int { NORM_NONE = 0, NORM_RMS = 1, NORM_LAYER = 2 };
 
 constexpr int NORM_MAX_DIM = 16384;
-constexpr int NORM_BWD_CTAS = 296;  // CTAs of the gradient kernel (two on each of 148 SMs): bounds its workspace
+constexpr int NORM_FWD_CTAS_PER_SM = 4, NORM_BWD_CTAS_PER_SM = 3;  // resident CTAs that rings are sized for
+constexpr int NORM_BWD_CTAS = 148 * NORM_BWD_CTAS_PER_SM;          // the gradient's CTAs: bounds its workspace
 
 struct NormVectors {  // fp32; gate, scale, shift [groups, dim], the rest [dim]; null where absent
     const float *gate, *scale, *shift, *pre_w, *pre_b, *post_w, *post_b;
@@ -23,11 +24,14 @@ struct NormArgs {
     void *dx, *dy;
     NormVectors v;
     float *dgate, *dscale, *dshift, *dpre_w, *dpre_b, *dpost_w, *dpost_b;
-    float* part;  // gradient: [slot][4][dim8] partial column sums; slot = CTA + group
+    float* part;    // gradient: [slot][4][dim8] partial column sums; slot = CTA + group
+    float* part_w;  // [CTA][4][dim8]: the same times 1 + scale or the gate, for the weights' gradients
+    bool weights;   // any of those is wanted
+    int* err;       // device error word (an expired bounded wait)
     long long rows, per_group;
     int dim, pre, post;
     float eps, alpha;
-    long long rows_per_cta;  // gradient: consecutive rows of a CTA
+    long long rows_per_cta;  // consecutive rows of a CTA
     int n_cta;
 };
 

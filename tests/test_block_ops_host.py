@@ -124,7 +124,7 @@ def test_norm_refusals():
 def test_norm_bwd_refusals():
     s = L.NormGateShape.make(4, 64, post="rms")
     need = L.lf_norm_gate_bwd_workspace(s)
-    assert need == (4 + 1) * 4 * 64 * 4
+    assert need == (4 + 4 + 1) * 4 * 64 * 4
 
     def f(x=p, y=p, dr=p, dh=p, dx=p, dy=p, v=None, g=None, ws=p, n=need, s=s):
         ref = lambda t: None if t is None else ctypes.byref(t)  # noqa: E731
@@ -142,7 +142,7 @@ def test_norm_bwd_refusals():
     with pytest.raises(L.LfError):
         L.lf_norm_gate_bwd_workspace(L.NormGateShape.make(4, 0))
     big = L.NormGateShape.make(10 ** 6, 100, rows_per_group=1 << 62)
-    assert L.lf_norm_gate_bwd_workspace(big) == (296 + 1) * 4 * 104 * 4
+    assert L.lf_norm_gate_bwd_workspace(big) == (444 + 444 + 1) * 4 * 104 * 4
 
 
 # ---------------------------------------------------------------- attention gradient
