@@ -114,11 +114,24 @@ __device__ __forceinline__ void load_param(const float* p, int col, int dim, boo
 
 constexpr int MAX_TEAMS = 8, MAX_STAGES = 4;
 
-// Row sums over a team of whole warps: two values at once, in a fixed order. Consecutive calls
-// alternate between two buffers, so one barrier a call is enough.
+// (d0, d1) = (a0, a1) * (b0, b1) + (c0, c1), packed
+__device__ __forceinline__ void ffma2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0, float c1)
+{
+    asm("{\n\t.reg .b64 ra, rb, rc;\n\t"
+        "mov.b64 ra, {%2, %3};\n\t"
+        "mov.b64 rb, {%4, %5};\n\t"
+        "mov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rc, ra, rb, rc;\n\t"
+        "mov.b64 {%0, %1}, rc;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+
+// Row sums over a team of whole warps, in a fixed order. Consecutive calls alternate between two
+// buffers, so one barrier a call is enough; unused places of a buffer stay zero.
 struct Team {
-    float (*red)[2][32];  // [2 buffers][2 values][warps of the CTA]
-    int warp0, warps, warp, lane, bar, threads, phase;
+    float (*red)[2][16];  // this team's [2 buffers][2 values][warps]
+    int warps, warp, lane, bar, threads, phase;
 
     __device__ __forceinline__ void sync()
     {
@@ -126,12 +139,24 @@ struct Team {
         else named_bar_sync(bar, threads);
     }
 
+    __device__ __forceinline__ float gather(int which)
+    {
+        const float4* f = reinterpret_cast<const float4*>(red[phase][which]);
+        const float4 u = f[0], v = f[1];
+        float s = ((u.x + u.y) + (u.z + u.w)) + ((v.x + v.y) + (v.z + v.w));
+        if (warps > 8) {
+            const float4 w = f[2], x = f[3];
+            s += ((w.x + w.y) + (w.z + w.w)) + ((x.x + x.y) + (x.z + x.w));
+        }
+        return s;
+    }
+
     __device__ __forceinline__ void sum(float& p, float& q)
     {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            p += __shfl_xor_sync(0xffffffffu, p, o);
-            q += __shfl_xor_sync(0xffffffffu, q, o);
+            const float a = __shfl_xor_sync(0xffffffffu, p, o), b = __shfl_xor_sync(0xffffffffu, q, o);
+            fadd2_acc(p, q, a, b);
         }
         if (warps == 1) return;
         if (lane == 0) {
@@ -139,11 +164,8 @@ struct Team {
             red[phase][1][warp] = q;
         }
         named_bar_sync(bar, threads);
-        p = q = 0.f;
-        for (int w = 0; w < warps; ++w) {
-            p += red[phase][0][warp0 + w];
-            q += red[phase][1][warp0 + w];
-        }
+        p = gather(0);
+        q = gather(1);
         phase ^= 1;
     }
 
@@ -154,57 +176,62 @@ struct Team {
         if (warps == 1) return;
         if (lane == 0) red[phase][0][warp] = p;
         named_bar_sync(bar, threads);
-        p = 0.f;
-        for (int w = 0; w < warps; ++w) p += red[phase][0][warp0 + w];
+        p = gather(0);
         phase ^= 1;
     }
 };
 
-__device__ __forceinline__ Team make_team(float (*red)[2][32], int team_threads)
+__device__ __forceinline__ Team make_team(float (*red)[2][2][16], int team_threads)
 {
     Team t;
-    const int team = threadIdx.x / team_threads;
-    t.red = red;
+    const int team = threadIdx.x / team_threads, in = threadIdx.x - team * team_threads;
+    t.red = red[team];
     t.warps = team_threads >> 5;
-    t.warp = threadIdx.x >> 5;
-    t.warp0 = team * t.warps;
+    t.warp = in >> 5;
     t.lane = threadIdx.x & 31;
     t.bar = 1 + team;
     t.threads = team_threads;
     t.phase = 0;
+    for (int i = in; i < 2 * 2 * 16; i += team_threads) (&t.red[0][0][0])[i] = 0.f;
     return t;
 }
 
 // Normalises the row in place (t -> (t - mean) / deviation) and returns 1 / deviation.
-// Elements past dim are zero before and stay zero.
+// Elements past dim are zero before and stay zero; `mine[k]` of a group's eight are within dim.
 template <int NV>
-__device__ __forceinline__ float normalise(Team& team, float (&t)[NV][8], int kind, int dim, int col0, int stride, float eps)
+__device__ __forceinline__ float normalise(Team& team, float (&t)[NV][8], int kind, float inv, const int (&mine)[NV], float eps)
 {
-    const float inv = 1.0f / static_cast<float>(dim);
+    float a = 0.f, b = 0.f;
     if (kind == NORM_LAYER) {
-        float s = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s += t[k][i];
+            for (int i = 0; i < 8; i += 2) fadd2_acc(a, b, t[k][i], t[k][i + 1]);
+        float s = a + b;
         team.sum(s);
-        const float mean = s * inv;
+        const float mean = -s * inv;
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
+        for (int k = 0; k < NV; ++k) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t[k][i] = col0 + k * stride + i < dim ? t[k][i] - mean : 0.f;
+            for (int i = 0; i < 8; i += 2) fadd2_acc(t[k][i], t[k][i + 1], mean, mean);
+            if (mine[k] < 8) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) t[k][i] = i < mine[k] ? t[k][i] : 0.f;
+            }
+        }
+        a = b = 0.f;
     }
-    float q = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q = fmaf(t[k][i], t[k][i], q);
+        for (int i = 0; i < 8; i += 2) ffma2(a, b, t[k][i], t[k][i + 1], t[k][i], t[k][i + 1], a, b);
+    float q = a + b;
     team.sum(q);
-    const float rs = 1.0f / sqrtf(q * inv + eps);
+    const float rs = rsqrtf(fmaf(q, inv, eps));
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t[k][i] *= rs;
+        for (int i = 0; i < 8; i += 2) fmul2(t[k][i], t[k][i + 1], rs, rs);
     return rs;
 }
 
@@ -226,7 +253,7 @@ struct Rows {
     uint32_t stage_bytes;
     uint8_t* ring;
     uint64_t* full;
-    int stages, used;
+    int stages, slot, parity;  // the next row's stage and its phase
     long long step, end;
     bool leader;
 
@@ -243,7 +270,7 @@ struct Rows {
 
     __device__ __forceinline__ void start(long long first)
     {
-        used = 0;
+        slot = parity = 0;
         if (leader)
             for (int s = 0; s < stages; ++s)
                 if (first + s * step < end) issue(first + s * step, s);
@@ -252,16 +279,18 @@ struct Rows {
     // Waits for the next row; its stage's address.
     __device__ __forceinline__ const uint8_t* wait(volatile int* abort_flag, int* err, bool* ok)
     {
-        const int s = used % stages;
-        *ok = mbar_wait(&full[s], (used / stages) & 1, abort_flag, err, 0x70);
-        return ring + s * stage_bytes;
+        *ok = mbar_wait(&full[slot], parity, abort_flag, err, 0x70);
+        return ring + slot * stage_bytes;
     }
 
     // The whole team has read `row`'s stage: its next use is filled.
     __device__ __forceinline__ void release(long long row)
     {
-        if (leader && row + stages * step < end) issue(row + stages * step, used % stages);
-        ++used;
+        if (leader && row + stages * step < end) issue(row + stages * step, slot);
+        if (++slot == stages) {
+            slot = 0;
+            parity ^= 1;
+        }
     }
 
     // After an expired wait: every copy issued lands before the CTA leaves.
@@ -306,12 +335,12 @@ __device__ __forceinline__ Raw8<T> stage_raw(const uint8_t* stage, uint32_t at, 
 // Registers a thread: what lets NORM_FWD_CTAS_PER_SM and NORM_BWD_CTAS_PER_SM CTAs of 192 threads
 // (1536 columns) share an SM; all there are where one CTA has the SM to itself.
 template <int NV> constexpr int FWD_REGS = NV == 1 ? 80 : 128;
-template <int NV> constexpr int BWD_REGS = NV == 1 ? 112 : 128;
+template <int NV> constexpr int BWD_REGS = NV == 1 ? 96 : 128;
 
 template <typename TX, typename TY, int NV>
 __global__ void __maxnreg__(FWD_REGS<NV>) norm_fwd_kernel(const NormArgs a, int team_threads, int stages, bool al)
 {
-    __shared__ float red[2][2][32];
+    __shared__ __align__(16) float red[MAX_TEAMS][2][2][16];
     __shared__ uint64_t full[MAX_TEAMS * MAX_STAGES];
     __shared__ int abort_word;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -333,7 +362,11 @@ __global__ void __maxnreg__(FWD_REGS<NV>) norm_fwd_kernel(const NormArgs a, int 
     Rows<2> in = make_rows<2>(src, esize, dim, smem, full, stages, ti, tt, teams, r1);
     in.start(r0 + ti);
 
-    long long group = -1;
+    const float inv = 1.0f / static_cast<float>(dim);
+    int mine[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) mine[k] = min(max(dim - (col0 + k * stride), 0), 8);
+    long long group_end = 0;  // rows below it share the vectors in registers
     float g2[NV][8], b2[NV][8], s1[NV][8], t1[NV][8];  // r = alpha x + m g2 + b2, h = n s1 + t1
     for (long long row = r0 + ti; row < r1; row += teams) {
         Raw8<TX> xr[NV];
@@ -359,9 +392,9 @@ __global__ void __maxnreg__(FWD_REGS<NV>) norm_fwd_kernel(const NormArgs a, int 
                 if (a.y) yr[k] = load_raw(static_cast<const TY*>(a.y) + row * dim, col0 + k * stride, dim, al);
             }
         }
-        if (row / a.per_group != group) {
-            group = row / a.per_group;
-            const long long g = group * dim;
+        if (row >= group_end) {
+            const long long group = row / a.per_group, g = group * dim;
+            group_end = (group + 1) * a.per_group;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int col = col0 + k * stride;
@@ -391,36 +424,42 @@ __global__ void __maxnreg__(FWD_REGS<NV>) norm_fwd_kernel(const NormArgs a, int 
         if (a.y) {
 #pragma unroll
             for (int k = 0; k < NV; ++k) unpack8(yr[k], t[k]);
-            if (a.post != NORM_NONE) normalise<NV>(team, t, a.post, dim, col0, stride, a.eps);
+            if (a.post != NORM_NONE) normalise<NV>(team, t, a.post, inv, mine, a.eps);
         }
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             float x[8];
             unpack8(xr[k], x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] *= a.alpha;
-                t[k][i] = a.y ? fmaf(g2[k][i], t[k][i], x[i] + b2[k][i]) : x[i];
+            for (int i = 0; i < 8; i += 2) {
+                if (a.y) {
+                    ffma2(x[i], x[i + 1], x[i], x[i + 1], a.alpha, a.alpha, b2[k][i], b2[k][i + 1]);
+                    ffma2(t[k][i], t[k][i + 1], g2[k][i], g2[k][i + 1], t[k][i], t[k][i + 1], x[i], x[i + 1]);
+                } else {
+                    t[k][i] = a.alpha * x[i];
+                    t[k][i + 1] = a.alpha * x[i + 1];
+                }
             }
             if (a.r) store8(static_cast<TX*>(a.r) + row * dim, col0 + k * stride, dim, al, t[k]);
         }
         if (!a.h) continue;
-        normalise<NV>(team, t, a.pre, dim, col0, stride, a.eps);
+        normalise<NV>(team, t, a.pre, inv, mine, a.eps);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) t[k][i] = fmaf(t[k][i], s1[k][i], t1[k][i]);
+            for (int i = 0; i < 8; i += 2)
+                ffma2(t[k][i], t[k][i + 1], t[k][i], t[k][i + 1], s1[k][i], s1[k][i + 1], t1[k][i], t1[k][i + 1]);
             store8(static_cast<TY*>(a.h) + row * dim, col0 + k * stride, dim, al, t[k]);
         }
     }
 }
 
-// A[j] of the header, and how many of the four are kept: A3 (sum dr') only where the post
-// norm has a bias or its gradient is wanted.
-template <typename TX, typename TY, int NV>
+// BIAS: the post norm has a bias, or its gradient is wanted; without it b2 and A3 (sum dr') need
+// no registers.
+template <typename TX, typename TY, int NV, bool BIAS>
 __global__ void __maxnreg__(BWD_REGS<NV>) norm_bwd_kernel(const NormArgs a, int team_threads, int stages, bool al)
 {
-    __shared__ float red[2][2][32];
+    __shared__ __align__(16) float red[MAX_TEAMS][2][2][16];
     __shared__ uint64_t full[MAX_TEAMS * MAX_STAGES];
     __shared__ int abort_word;
     extern __shared__ __align__(16) uint8_t smem[];  // the rings, then [teams - 1][dim8] floats
@@ -446,24 +485,28 @@ __global__ void __maxnreg__(BWD_REGS<NV>) norm_bwd_kernel(const NormArgs a, int 
     float* fold = reinterpret_cast<float*>(smem + static_cast<size_t>(teams) * stages * in.stage_bytes);
     float* part_w = a.part_w + static_cast<long long>(blockIdx.x) * 4 * dim8;
 
+    int mine[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) mine[k] = min(max(dim - (col0 + k * stride), 0), 8);
     long long row = r0 + ti;
     bool broken = false;
     for (long long seg = r0; seg < r1;) {
         const long long gi = seg / a.per_group;
         const long long seg_end = min(r1, (gi + 1) * a.per_group);
         const long long g = gi * dim;
-        float g2[NV][8], b2[NV][8], s1[NV][8];  // u gate = m g2 + b2; dn = dh s1
+        float g2[NV][8], b2[BIAS ? NV : 1][8], s1[NV][8];  // u gate = m g2 + b2; dn = dh s1
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int col = col0 + k * stride;
             float p[8];
             load_param(a.v.gate ? a.v.gate + g : nullptr, col, dim, al, 1.f, p);
             load_param(a.v.post_w, col, dim, al, 1.f, g2[k]);
-            load_param(a.v.post_b, col, dim, al, 0.f, b2[k]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                g2[k][i] *= p[i];
-                b2[k][i] *= p[i];
+            for (int i = 0; i < 8; ++i) g2[k][i] *= p[i];
+            if constexpr (BIAS) {
+                load_param(a.v.post_b, col, dim, al, 0.f, b2[k]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) b2[k][i] *= p[i];
             }
             load_param(a.v.scale ? a.v.scale + g : nullptr, col, dim, al, 0.f, p);
             load_param(a.v.pre_w, col, dim, al, 1.f, s1[k]);
@@ -500,47 +543,61 @@ __global__ void __maxnreg__(BWD_REGS<NV>) norm_bwd_kernel(const NormArgs a, int 
             if (a.y) {
 #pragma unroll
                 for (int k = 0; k < NV; ++k) unpack8(load_raw(y_row, col0 + k * stride, dim, al), m[k]);
-                if (a.post != NORM_NONE) rs2 = normalise<NV>(team, m, a.post, dim, col0, stride, a.eps);
+                if (a.post != NORM_NONE) rs2 = normalise<NV>(team, m, a.post, inv, mine, a.eps);
             }
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 unpack8(load_raw(x_row, col0 + k * stride, dim, al), n[k]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    n[k][i] *= a.alpha;
-                    if (a.y) n[k][i] = fmaf(g2[k][i], m[k][i], n[k][i] + b2[k][i]);
+                for (int i = 0; i < 8; i += 2) {
+                    if constexpr (BIAS)
+                        ffma2(n[k][i], n[k][i + 1], n[k][i], n[k][i + 1], a.alpha, a.alpha, b2[k][i], b2[k][i + 1]);
+                    else
+                        fmul2(n[k][i], n[k][i + 1], a.alpha, a.alpha);
+                    if (a.y)
+                        ffma2(n[k][i], n[k][i + 1], g2[k][i], g2[k][i + 1], m[k][i], m[k][i + 1], n[k][i], n[k][i + 1]);
                 }
             }
             float q1 = 0.f, q2 = 0.f;
             if (a.dh) {
-                rs1 = normalise<NV>(team, n, a.pre, dim, col0, stride, a.eps);
+                rs1 = normalise<NV>(team, n, a.pre, inv, mine, a.eps);
+                float q3 = 0.f, q4 = 0.f;
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
                     unpack8(load_raw(dh_row, col0 + k * stride, dim, al), d[k]);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        A[0][k][i] += d[k][i];
-                        A[1][k][i] = fmaf(d[k][i], n[k][i], A[1][k][i]);
-                        d[k][i] *= s1[k][i];
-                        q1 += d[k][i];
-                        q2 = fmaf(d[k][i], n[k][i], q2);
+                    for (int i = 0; i < 8; i += 2) {
+                        fadd2_acc(A[0][k][i], A[0][k][i + 1], d[k][i], d[k][i + 1]);
+                        ffma2(A[1][k][i], A[1][k][i + 1], d[k][i], d[k][i + 1], n[k][i], n[k][i + 1], A[1][k][i], A[1][k][i + 1]);
+                        fmul2(d[k][i], d[k][i + 1], s1[k][i], s1[k][i + 1]);
+                        fadd2_acc(q1, q3, d[k][i], d[k][i + 1]);
+                        ffma2(q2, q4, d[k][i], d[k][i + 1], n[k][i], n[k][i + 1], q2, q4);
                     }
                 }
+                q1 += q3;
+                q2 += q4;
                 team.sum(q1, q2);
-                q1 = a.pre == NORM_LAYER ? q1 * inv : 0.f;
-                q2 *= inv;
+                // minus rs1 times the means
+                q1 = a.pre == NORM_LAYER ? q1 * inv * -rs1 : 0.f;
+                q2 *= inv * -rs1;
             }
             // dr' in d
-            float p1 = 0.f, p2 = 0.f;
+            float p1 = 0.f, p2 = 0.f, p3 = 0.f, p4 = 0.f;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int col = col0 + k * stride;
-                float p[8];
+                float p[8] = {};
                 if (a.dr) unpack8(load_raw(dr_row, col, dim, al), p);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float dn = a.dh ? rs1 * (d[k][i] - q1 - n[k][i] * q2) : 0.f;
-                    d[k][i] = (a.dr ? p[i] : 0.f) + dn;
+                for (int i = 0; i < 8; i += 2) {
+                    if (a.dh) {
+                        fadd2_acc(p[i], p[i + 1], q1, q1);
+                        ffma2(p[i], p[i + 1], d[k][i], d[k][i + 1], rs1, rs1, p[i], p[i + 1]);
+                        ffma2(d[k][i], d[k][i + 1], n[k][i], n[k][i + 1], q2, q2, p[i], p[i + 1]);
+                    } else {
+                        d[k][i] = p[i];
+                        d[k][i + 1] = p[i + 1];
+                    }
                 }
                 if (a.dx) {
 #pragma unroll
@@ -549,12 +606,12 @@ __global__ void __maxnreg__(BWD_REGS<NV>) norm_bwd_kernel(const NormArgs a, int 
                 }
                 if (a.y) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        A[2][k][i] += d[k][i];
-                        A[3][k][i] = fmaf(d[k][i], m[k][i], A[3][k][i]);
-                        d[k][i] *= g2[k][i];  // dm (zero past dim, as g2 is)
-                        p1 += d[k][i];
-                        p2 = fmaf(d[k][i], m[k][i], p2);
+                    for (int i = 0; i < 8; i += 2) {
+                        if constexpr (BIAS) fadd2_acc(A[2][k][i], A[2][k][i + 1], d[k][i], d[k][i + 1]);
+                        ffma2(A[3][k][i], A[3][k][i + 1], d[k][i], d[k][i + 1], m[k][i], m[k][i + 1], A[3][k][i], A[3][k][i + 1]);
+                        fmul2(d[k][i], d[k][i + 1], g2[k][i], g2[k][i + 1]);  // dm (zero past dim, as g2 is)
+                        fadd2_acc(p1, p3, d[k][i], d[k][i + 1]);
+                        ffma2(p2, p4, d[k][i], d[k][i + 1], m[k][i], m[k][i + 1], p2, p4);
                     }
                 }
             }
@@ -564,13 +621,18 @@ __global__ void __maxnreg__(BWD_REGS<NV>) norm_bwd_kernel(const NormArgs a, int 
             }
             if (!a.dy) continue;
             if (a.post != NORM_NONE) {
+                p1 += p3;
+                p2 += p4;
                 team.sum(p1, p2);
-                p1 = a.post == NORM_LAYER ? p1 * inv : 0.f;
-                p2 *= inv;
+                p1 = a.post == NORM_LAYER ? p1 * inv * -rs2 : 0.f;
+                p2 *= inv * -rs2;
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) d[k][i] = rs2 * (d[k][i] - p1 - m[k][i] * p2);
+                    for (int i = 0; i < 8; i += 2) {
+                        ffma2(d[k][i], d[k][i + 1], d[k][i], d[k][i + 1], rs2, rs2, p1, p1);
+                        ffma2(d[k][i], d[k][i + 1], m[k][i], m[k][i + 1], p2, p2, d[k][i], d[k][i + 1]);
+                    }
             }
 #pragma unroll
             for (int k = 0; k < NV; ++k) store8(static_cast<TY*>(a.dy) + at, col0 + k * stride, dim, al, d[k]);
@@ -630,28 +692,37 @@ __global__ void __maxnreg__(BWD_REGS<NV>) norm_bwd_kernel(const NormArgs a, int 
     }
 }
 
-constexpr int FIN_COLS = 32, FIN_ROWS = 32;
+constexpr int FIN_COLS = 32, FIN_ROWS = 32, FIN_GROUPS = 4;
 
-// Adds the partial rows up: blockIdx.y < groups is a group's dgate, dscale and dshift, the
-// last one the weights' gradients over all CTAs. A CTA takes 32 columns, 32 threads each.
+// Adds the partial rows up. A CTA takes 32 columns of four consecutive groups (dgate, dscale,
+// dshift; 8 threads a column and group), or, blockIdx.y being the last, of the weights' gradients
+// over all CTAs (32 threads a column).
 __global__ void __launch_bounds__(FIN_COLS * FIN_ROWS) norm_bwd_finish_kernel(const NormArgs a, long long groups)
 {
     __shared__ float red[4][FIN_ROWS][FIN_COLS];
     const int c = threadIdx.x % FIN_COLS, j = threadIdx.x / FIN_COLS;
     const int col = blockIdx.x * FIN_COLS + c;
     const int dim8 = (a.dim + 7) & ~7;
-    for (long long item = blockIdx.y; item < groups + (a.weights ? 1 : 0); item += gridDim.y) {
-        const bool all = item == groups;
+    const long long batches = (groups + FIN_GROUPS - 1) / FIN_GROUPS;
+    for (long long batch = blockIdx.y; batch < batches + (a.weights ? 1 : 0); batch += gridDim.y) {
+        const bool all = batch == batches;
+        const int rows = all ? FIN_ROWS : FIN_ROWS / FIN_GROUPS, first = j % rows;
+        const long long item = all ? 0 : batch * FIN_GROUPS + j / rows;
         // consecutive partial rows: a group's are those of the CTAs that met it
-        const long long row0 = all ? 0 : item * a.per_group;
-        const long long row1 = all ? a.rows : min(a.rows, row0 + a.per_group);
-        const long long c0 = row0 / a.rows_per_cta;
-        const int n = static_cast<int>((row1 - 1) / a.rows_per_cta - c0) + 1;
-        const float* base = (all ? a.part_w : a.part + (c0 + item) * 4 * dim8) + col;
+        int n = 0;
+        const float* base = a.part_w + col;
+        if (all) {
+            n = a.n_cta;
+        } else if (item < groups) {
+            const long long row0 = item * a.per_group, row1 = min(a.rows, row0 + a.per_group);
+            const long long c0 = row0 / a.rows_per_cta;
+            n = static_cast<int>((row1 - 1) / a.rows_per_cta - c0) + 1;
+            base = a.part + (c0 + item) * 4 * dim8 + col;
+        }
         float A[4] = {0.f, 0.f, 0.f, 0.f};
         if (col < a.dim) {
 #pragma unroll 4
-            for (int s = j; s < n; s += FIN_ROWS) {
+            for (int s = first; s < n; s += rows) {
                 const float* p = base + static_cast<long long>(s) * 4 * dim8;
                 A[0] += p[0];
                 A[1] += p[dim8];
@@ -663,15 +734,15 @@ __global__ void __launch_bounds__(FIN_COLS * FIN_ROWS) norm_bwd_finish_kernel(co
 #pragma unroll
         for (int i = 0; i < 4; ++i) red[i][j][c] = A[i];
         __syncthreads();
-        if (j < 4) {  // thread row j adds sum j
+        if (first < 4) {  // a group's thread row i adds its sum i
             float s = 0.f;
-#pragma unroll
-            for (int o = 0; o < FIN_ROWS; ++o) s += red[j][o][c];
-            red[j][0][c] = s;
+            for (int o = 0; o < rows; ++o) s += red[first][j - first + o][c];
+            __syncwarp();
+            red[first][j - first][c] = s;
         }
         __syncthreads();
-        if (j == 0 && col < a.dim) {
-            const float a1 = red[0][0][c], a2 = red[1][0][c], a3 = red[2][0][c], a4 = red[3][0][c];
+        if (first == 0 && col < a.dim && n > 0) {
+            const float a1 = red[0][j][c], a2 = red[1][j][c], a3 = red[2][j][c], a4 = red[3][j][c];
             if (all) {
                 if (a.dpre_w) a.dpre_w[col] = a2;
                 if (a.dpre_b) a.dpre_b[col] = a1;
@@ -743,13 +814,17 @@ cudaError_t launch_fwd(NormArgs a, const NormPlan& p, cudaStream_t s)
 template <typename TX, typename TY, int NV>
 cudaError_t launch_bwd(const NormArgs& a, const NormPlan& p, cudaStream_t s)
 {
-    cudaError_t e = allow_smem<norm_bwd_kernel<TX, TY, NV>>(p.smem);
+    const bool bias = a.v.post_b || a.dpost_b;
+    cudaError_t e = bias ? allow_smem<norm_bwd_kernel<TX, TY, NV, true>>(p.smem) : allow_smem<norm_bwd_kernel<TX, TY, NV, false>>(p.smem);
     if (e != cudaSuccess) return e;
-    norm_bwd_kernel<TX, TY, NV><<<a.n_cta, p.threads * p.teams, p.smem, s>>>(a, p.threads, p.stages, a.dim % 8 == 0);
+    if (bias)
+        norm_bwd_kernel<TX, TY, NV, true><<<a.n_cta, p.threads * p.teams, p.smem, s>>>(a, p.threads, p.stages, a.dim % 8 == 0);
+    else
+        norm_bwd_kernel<TX, TY, NV, false><<<a.n_cta, p.threads * p.teams, p.smem, s>>>(a, p.threads, p.stages, a.dim % 8 == 0);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (!a.dgate && !a.dscale && !a.dshift && !a.weights) return cudaSuccess;
     const long long groups = (a.rows + a.per_group - 1) / a.per_group;
-    const long long items = groups + (a.weights ? 1 : 0);
+    const long long items = (groups + FIN_GROUPS - 1) / FIN_GROUPS + (a.weights ? 1 : 0);
     norm_bwd_finish_kernel<<<dim3((a.dim + FIN_COLS - 1) / FIN_COLS, static_cast<unsigned>(std::min<long long>(items, 65535))),
                              FIN_COLS * FIN_ROWS, 0, s>>>(a, groups);
     return cudaGetLastError();
