@@ -9,9 +9,10 @@ import sys
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_HERE)
 SOURCES = ["lf_api.cu", "lf_pool.cu", "lf_select.cu", "lf_ivf.cu", "lf_quant.cu", "lf_attn.cu",
-           "lf_attn_bwd.cu", "lf_rope.cu", "lf_norm.cu"]
+           "lf_attn_bwd.cu", "lf_rope.cu", "lf_norm.cu",
+           "lf_norm_bwd.cu"]
 HEADERS = ["lf_device.cuh", "lf_internal.h", "lf_score.cuh", "lf_types.cuh", "lf_attn_bwd.h", "lf_rope.h",
-           "lf_norm.h"]
+           "lf_norm.h", "lf_norm_rows.cuh"]
 LIB = os.path.join(_HERE, "liblf_hsa.so")
 OBJ_DIR = os.path.join(_HERE, "_build")
 

@@ -10,8 +10,7 @@ namespace lf {
 enum : int { NORM_NONE = 0, NORM_RMS = 1, NORM_LAYER = 2 };
 
 constexpr int NORM_MAX_DIM = 16384;
-constexpr int NORM_FWD_CTAS_PER_SM = 4, NORM_BWD_CTAS_PER_SM = 3;  // resident CTAs that rings are sized for
-constexpr int NORM_BWD_CTAS = 148 * NORM_BWD_CTAS_PER_SM;          // the gradient's CTAs: bounds its workspace
+constexpr int NORM_BWD_CTAS = 148;  // the gradient's CTAs, one an SM: bounds its workspace
 
 struct NormVectors {  // fp32; gate, scale, shift [groups, dim], the rest [dim]; null where absent
     const float *gate, *scale, *shift, *pre_w, *pre_b, *post_w, *post_b;

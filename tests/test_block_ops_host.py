@@ -142,7 +142,7 @@ def test_norm_bwd_refusals():
     with pytest.raises(L.LfError):
         L.lf_norm_gate_bwd_workspace(L.NormGateShape.make(4, 0))
     big = L.NormGateShape.make(10 ** 6, 100, rows_per_group=1 << 62)
-    assert L.lf_norm_gate_bwd_workspace(big) == (444 + 444 + 1) * 4 * 104 * 4
+    assert L.lf_norm_gate_bwd_workspace(big) == (148 + 148 + 1) * 4 * 104 * 4
 
 
 # ---------------------------------------------------------------- attention gradient
