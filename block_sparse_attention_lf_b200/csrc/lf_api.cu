@@ -751,16 +751,18 @@ lf_status lf_rope(const lf_rope_plan* plan, int32_t batch, int32_t tokens, int32
     if (batch == 0 || tokens == 0) return LF_OK;
     if (static_cast<long long>(batch) * tokens * D >= (1ll << 31)) return LF_ERR_SHAPE;
     if (!positions) return LF_ERR_NULL;
-    const int size = dtype == LF_F32 ? 4 : 2, elems = 16 / size;
+    const int size = dtype == LF_F32 ? 4 : 2;
     if ((reinterpret_cast<uintptr_t>(positions) & 3u) != 0) return LF_ERR_ALIGN;
     lf::RopeArgs a = {};
     const bool half = plan->layout == LF_ROPE_HALF;
-    bool vec = (half ? rot / 2 : rot) % elems == 0 && (D - rot) % elems == 0;
+    // the widest load that every span, pointer and stride is a whole number of: their common factor
+    // of two, as a set of bits
+    uint64_t all = static_cast<uint64_t>(half ? rot / 2 : rot) | static_cast<uint64_t>(D - rot) | static_cast<uint64_t>(16 / size);
     for (int k = 0; k < n_io; ++k) {
         if (!io[k].x || !io[k].out) return LF_ERR_NULL;
         const uintptr_t both = reinterpret_cast<uintptr_t>(io[k].x) | reinterpret_cast<uintptr_t>(io[k].out);
         if (both % size != 0) return LF_ERR_ALIGN;
-        vec = vec && both % 16 == 0;
+        all |= both / size;
         const int extent[3] = {batch, io[k].heads, tokens};
         a.io[k].x = io[k].x;
         a.io[k].out = io[k].out;
@@ -771,7 +773,7 @@ lf_status lf_rope(const lf_rope_plan* plan, int32_t batch, int32_t tokens, int32
             if (xs < 0 || os < 0 || (os == 0 && extent[i] > 1)) return LF_ERR_ARG;
             a.io[k].xs[i] = extent[i] > 1 ? xs : 0;
             a.io[k].os[i] = extent[i] > 1 ? os : 0;
-            vec = vec && a.io[k].xs[i] % elems == 0 && a.io[k].os[i] % elems == 0;
+            all |= static_cast<uint64_t>(a.io[k].xs[i]) | static_cast<uint64_t>(a.io[k].os[i]);
         }
     }
     a.n_io = n_io;
@@ -792,7 +794,8 @@ lf_status lf_rope(const lf_rope_plan* plan, int32_t batch, int32_t tokens, int32
         if (!std::isfinite(plan->turns[p])) return LF_ERR_ARG;
         a.turns[p] = plan->turns[p];
     }
-    return launch_status(lf::launch_rope(a, dtype, half, vec, static_cast<cudaStream_t>(stream)));
+    const int elems = static_cast<int>(all & (~all + 1));  // the lowest bit set; at most 16 / size
+    return launch_status(lf::launch_rope(a, dtype, half, elems, static_cast<cudaStream_t>(stream)));
 }
 
 namespace {

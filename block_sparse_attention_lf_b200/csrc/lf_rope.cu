@@ -14,8 +14,11 @@
 // unit (a 16-byte vector, or two half a head apart) once and uses them for every head
 // it takes, so the fp64 work is spread over heads * tensors vectors.
 //
-// Memory-bound: each element is read and written once. A unit is one 16-byte vector
-// wherever pointers, strides and spans allow it; otherwise one pair at a time.
+// Memory-bound: each element is read and written once. A unit is the widest vector (16, 8, 4 or
+// 2 bytes) that pointers, strides and spans allow; a thread asks for several heads' units before
+// it forms the angles, which take longer than a head's arithmetic, and for the next heads' before
+// it stores these. Frequencies are staged in shared memory: lanes need different ones, which the
+// constant bank would serve one by one.
 #include "lf_rope.h"
 #include "lf_types.cuh"
 
@@ -24,51 +27,50 @@ namespace {
 
 constexpr int ROPE_THREADS = 256;
 
-__device__ __forceinline__ void turn_of(double turns, int pos, float& c, float& s)
+__device__ __forceinline__ void turn_of(double turns, double pos, float& c, float& s)
 {
-    double t = static_cast<double>(pos) * turns;
-    t -= rint(t);
-    sincospif(2.0f * static_cast<float>(t), &s, &c);
+    // t - rint(t) by adding and taking off 1.5 * 2^52 (|t| < 2^31)
+    const double t = pos * turns;
+    const double whole = __dadd_rn(__dadd_rn(t, 6755399441055744.0), -6755399441055744.0);
+    sincospif(2.0f * static_cast<float>(t - whole), &s, &c);
 }
 
-// Elements of a unit and how many units a head has: rotated ones first, then copied ones.
-// VEC: a unit is a 16-byte vector (interleaved, copied) or two of them half a head's rotated
-// part apart (half). Otherwise a pair, or one copied element.
-template <typename T, bool HALF, bool VEC>
+template <int BYTES> struct RopeWord;
+template <> struct RopeWord<16> { using type = uint4; };
+template <> struct RopeWord<8> { using type = uint2; };
+template <> struct RopeWord<4> { using type = uint32_t; };
+template <> struct RopeWord<2> { using type = uint16_t; };
+
+// E elements of T as loaded.
+template <typename T, int E>
+struct Chunk {
+    typename RopeWord<E * static_cast<int>(sizeof(T))>::type w;
+    __device__ __forceinline__ void load(const T* p) { w = *reinterpret_cast<const decltype(w)*>(p); }
+    __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<decltype(w)*>(p) = w; }
+    __device__ __forceinline__ float get(int i) const { return to_f32(reinterpret_cast<const T*>(&w)[i]); }
+    __device__ __forceinline__ void set(int i, float x) { reinterpret_cast<T*>(&w)[i] = from_f32<T>(x); }
+};
+
+// A unit of E elements and, where its pairs' second members lie apart (half layout, or single
+// elements), the E elements that hold them.
+template <typename T, bool HALF, int E>
 struct RopeUnits {
-    static constexpr int E = VEC ? VEC_ELEMS<T> : 1;              // elements of a load
-    static constexpr int PAIRS = HALF ? E : (VEC ? E / 2 : 1);    // pairs of a rotated unit
-    static constexpr int SPAN = HALF ? E : (VEC ? E : 2);         // elements between rotated units' starts
+    static constexpr bool TWO = HALF || E == 1;
+    static constexpr int PAIRS = TWO ? E : E / 2;               // pairs of a rotated unit
+    static constexpr int SPAN = !HALF && E == 1 ? 2 : E;        // elements between rotated units' starts
     __host__ __device__ static int rotated(int rot) { return (HALF ? rot / 2 : rot) / SPAN; }
     __host__ __device__ static int all(int D, int rot) { return rotated(rot) + (D - rot) / E; }
 };
 
-template <typename T, int E>
-__device__ __forceinline__ void load_elems(float (&v)[E], const T* p)
-{
-    if constexpr (E == 1)
-        v[0] = to_f32(*p);
-    else
-        unpack<T>(*reinterpret_cast<const uint4*>(p), v);
-}
-
-template <typename T, int E>
-__device__ __forceinline__ void store_elems(T* p, const float (&v)[E])
-{
-    if constexpr (E == 1)
-        *p = from_f32<T>(v[0]);
-    else
-        *reinterpret_cast<uint4*>(p) = pack<T>(v);
-}
-
-// The two operands of a rotated unit: in the half layout two loads, interleaved one load
-// whose even and odd elements are the pair's members.
-template <typename T, bool HALF, bool VEC>
+template <typename T, bool HALF, int E>
 __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constant__ RopeArgs a)
 {
-    using U = RopeUnits<T, HALF, VEC>;
-    constexpr int E = U::E, NP = U::PAIRS;
-    constexpr int UNROLL = 4;  // heads loaded before any is stored
+    using U = RopeUnits<T, HALF, E>;
+    constexpr int NP = U::PAIRS;
+    constexpr int AHEAD = 3;  // heads asked for at once (1, 2, 3, 4: 39.9, 35.0, 34.5, 35.3 us for 32760 tokens of 12 x 128 bf16)
+    __shared__ double turns[ROPE_MAX_PAIRS];
+    for (int i = threadIdx.x; i < a.rot_dim / 2; i += ROPE_THREADS) turns[i] = a.turns[i];
+    __syncthreads();
     const int rot_units = U::rotated(a.rot_dim), units = U::all(a.head_dim, a.rot_dim);
     const unsigned item = blockIdx.x * ROPE_THREADS + threadIdx.x;
     const unsigned bt = item / units;
@@ -77,83 +79,88 @@ __global__ void __launch_bounds__(ROPE_THREADS) rope_kernel(const __grid_constan
     const int b = bt / a.tokens, t = bt - b * a.tokens;
     const bool turned = u < rot_units;
     const int e0 = turned ? u * U::SPAN : a.rot_dim + (u - rot_units) * E;  // first element
-    const int half = a.rot_dim >> 1;
+    const int apart = HALF ? a.rot_dim >> 1 : 1;
+    const bool two = U::TWO && turned;
+
+    // This thread's heads: `left` of them from head h0 of tensor k on.
+    int h0 = blockIdx.y * a.heads_per_thread, left = a.heads_per_thread, k = 0;
+    while (h0 >= a.io[k].heads) h0 -= a.io[k++].heads;
+    Chunk<T, E> va[AHEAD], vb[AHEAD];
+    auto ask = [&](const RopeIo& io, int h, int n) {  // heads [h, h + n) of a tensor, n <= AHEAD
+        const T* x = static_cast<const T*>(io.x) + b * io.xs[0] + h * io.xs[1] + t * io.xs[2] + e0;
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (i < n) {
+                va[i].load(x + i * io.xs[1]);
+                if (U::TWO && two) vb[i].load(x + i * io.xs[1] + apart);
+            }
+    };
+    int n = min(min(left, a.io[k].heads - h0), AHEAD);
+    ask(a.io[k], h0, n);
 
     float c[NP], s[NP];
     if (turned) {
         const int* pos = a.positions + b * a.pos_batch + static_cast<long long>(t) * a.n_axes;
+        const double p0 = __ldg(pos);
+        const double p1 = a.n_axes > 1 ? __ldg(pos + 1) : 0, p2 = a.n_axes > 2 ? __ldg(pos + 2) : 0;
+        const float sa = a.backward ? -a.amplitude : a.amplitude;
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             const int p = u * NP + i;
-            const int ax = (p >= a.axis_end[0]) + (p >= a.axis_end[1]);
-            turn_of(a.turns[p], __ldg(pos + ax), c[i], s[i]);
+            turn_of(turns[p], p < a.axis_end[0] ? p0 : (p < a.axis_end[1] ? p1 : p2), c[i], s[i]);
             c[i] *= a.amplitude;
-            s[i] *= a.backward ? -a.amplitude : a.amplitude;
+            s[i] *= sa;
         }
     }
-    int h0 = blockIdx.y * a.heads_per_thread;
-    int left = a.heads_per_thread;
-    for (int k = 0; k < a.n_io && left > 0; ++k) {
+    while (n > 0) {
         const RopeIo& io = a.io[k];
-        if (h0 >= io.heads) {
-            h0 -= io.heads;
-            continue;
-        }
-        const int n = min(left, io.heads - h0);
-        const T* x = static_cast<const T*>(io.x) + b * io.xs[0] + h0 * io.xs[1] + t * io.xs[2] + e0;
         T* o = static_cast<T*>(io.out) + b * io.os[0] + h0 * io.os[1] + t * io.os[2] + e0;
+        Chunk<T, E> ra[AHEAD], rb[AHEAD];
         const bool rotate = turned && io.rotate;
-        for (int h = 0; h < n; h += UNROLL) {
-            float va[UNROLL][E], vb[UNROLL][E];  // vb: the second operand (half layout, or the scalar pair's)
+        const long long step = io.os[1];
 #pragma unroll
-            for (int i = 0; i < UNROLL; ++i)
-                if (h + i < n) {
-                    const T* p = x + (h + i) * io.xs[1];
-                    load_elems<T, E>(va[i], p);
-                    if constexpr (HALF) {
-                        if (turned) load_elems<T, E>(vb[i], p + half);
-                    } else if constexpr (!VEC) {
-                        if (turned) load_elems<T, E>(vb[i], p + 1);
-                    }
-                }
+        for (int i = 0; i < AHEAD; ++i) {
+            ra[i] = va[i];
+            rb[i] = vb[i];
+        }
+        const int done = n;
+        // the next heads, before these are stored
+        left -= n;
+        h0 += n;
+        if (h0 == io.heads) {
+            h0 = 0;
+            ++k;
+        }
+        n = left > 0 && k < a.n_io ? min(min(left, a.io[k].heads - h0), AHEAD) : 0;
+        if (n > 0) ask(a.io[k], h0, n);
 #pragma unroll
-            for (int i = 0; i < UNROLL; ++i)
-                if (h + i < n) {
-                    T* p = o + (h + i) * io.os[1];
-                    if (rotate) {
-                        if constexpr (HALF || !VEC) {
+        for (int i = 0; i < AHEAD; ++i)
+            if (i < done) {
+                if (rotate) {
 #pragma unroll
-                            for (int j = 0; j < E; ++j) {
-                                const float xa = va[i][j], xb = vb[i][j];
-                                va[i][j] = xa * c[j] - xb * s[j];
-                                vb[i][j] = xa * s[j] + xb * c[j];
-                            }
+                    for (int j = 0; j < NP; ++j) {
+                        const float xa = U::TWO ? ra[i].get(j) : ra[i].get(2 * j);
+                        const float xb = U::TWO ? rb[i].get(j) : ra[i].get(2 * j + 1);
+                        const float ya = xa * c[j] - xb * s[j], yb = xa * s[j] + xb * c[j];
+                        if (U::TWO) {
+                            ra[i].set(j, ya);
+                            rb[i].set(j, yb);
                         } else {
-#pragma unroll
-                            for (int j = 0; j < NP; ++j) {
-                                const float xa = va[i][2 * j], xb = va[i][2 * j + 1];
-                                va[i][2 * j] = xa * c[j] - xb * s[j];
-                                va[i][2 * j + 1] = xa * s[j] + xb * c[j];
-                            }
+                            ra[i].set(2 * j, ya);
+                            ra[i].set(2 * j + 1, yb);
                         }
                     }
-                    store_elems<T, E>(p, va[i]);
-                    if constexpr (HALF) {
-                        if (turned) store_elems<T, E>(p + half, vb[i]);
-                    } else if constexpr (!VEC) {
-                        if (turned) store_elems<T, E>(p + 1, vb[i]);
-                    }
                 }
-        }
-        left -= n;
-        h0 = 0;
+                ra[i].store(o + i * step);
+                if (U::TWO && two) rb[i].store(o + i * step + apart);
+            }
     }
 }
 
-template <typename T, bool HALF, bool VEC>
+template <typename T, bool HALF, int E>
 cudaError_t launch_t(RopeArgs& a, cudaStream_t s)
 {
-    const long long items = static_cast<long long>(a.batch) * a.tokens * RopeUnits<T, HALF, VEC>::all(a.head_dim, a.rot_dim);
+    const long long items = static_cast<long long>(a.batch) * a.tokens * RopeUnits<T, HALF, E>::all(a.head_dim, a.rot_dim);
     int heads = 0;
     for (int k = 0; k < a.n_io; ++k) heads += a.io[k].heads;
     // Heads are spread over threads until the machine is full: 148 SMs * 1024 threads.
@@ -162,25 +169,34 @@ cudaError_t launch_t(RopeArgs& a, cudaStream_t s)
     a.heads_per_thread = (heads + groups - 1) / groups;
     const dim3 grid(static_cast<unsigned>((items + ROPE_THREADS - 1) / ROPE_THREADS),
                     static_cast<unsigned>((heads + a.heads_per_thread - 1) / a.heads_per_thread));
-    rope_kernel<T, HALF, VEC><<<grid, ROPE_THREADS, 0, s>>>(a);
+    rope_kernel<T, HALF, E><<<grid, ROPE_THREADS, 0, s>>>(a);
     return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t launch_l(RopeArgs& a, bool half_layout, bool vec, cudaStream_t s)
+template <typename T, bool HALF>
+cudaError_t launch_e(RopeArgs& a, int elems, cudaStream_t s)
 {
-    if (half_layout) return vec ? launch_t<T, true, true>(a, s) : launch_t<T, true, false>(a, s);
-    return vec ? launch_t<T, false, true>(a, s) : launch_t<T, false, false>(a, s);
+    if constexpr (sizeof(T) == 2) {
+        if (elems == 8) return launch_t<T, HALF, 8>(a, s);
+    }
+    if (elems == 4) return launch_t<T, HALF, 4>(a, s);
+    return elems == 2 ? launch_t<T, HALF, 2>(a, s) : launch_t<T, HALF, 1>(a, s);
+}
+
+template <typename T>
+cudaError_t launch_l(RopeArgs& a, bool half_layout, int elems, cudaStream_t s)
+{
+    return half_layout ? launch_e<T, true>(a, elems, s) : launch_e<T, false>(a, elems, s);
 }
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeArgs& a0, int dtype, bool half_layout, bool vec, cudaStream_t s)
+cudaError_t launch_rope(const RopeArgs& a0, int dtype, bool half_layout, int elems, cudaStream_t s)
 {
     RopeArgs a = a0;
-    if (dtype == DT_F32) return launch_l<float>(a, half_layout, vec, s);
-    if (dtype == DT_BF16) return launch_l<__nv_bfloat16>(a, half_layout, vec, s);
-    return launch_l<__half>(a, half_layout, vec, s);
+    if (dtype == DT_F32) return launch_l<float>(a, half_layout, elems, s);
+    if (dtype == DT_BF16) return launch_l<__nv_bfloat16>(a, half_layout, elems, s);
+    return launch_l<__half>(a, half_layout, elems, s);
 }
 
 }  // namespace lf

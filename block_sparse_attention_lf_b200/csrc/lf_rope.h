@@ -28,8 +28,8 @@ struct RopeArgs {
     double turns[ROPE_MAX_PAIRS];  // revolutions per position of each pair
 };
 
-// elem: bytes of an element (2 or 4); bf16 tells the two 2-byte types apart; vec: every pointer,
-// stride and span is a whole number of 16-byte vectors
-cudaError_t launch_rope(const RopeArgs& a, int dtype, bool half_layout, bool vec, cudaStream_t s);
+// elems: elements of a load (1, 2, 4 or 8; at most 16 bytes), which every pointer, stride and span
+// is a whole number of
+cudaError_t launch_rope(const RopeArgs& a, int dtype, bool half_layout, int elems, cudaStream_t s);
 
 }  // namespace lf
