@@ -120,19 +120,6 @@ __device__ __forceinline__ float neg_lse_log2(float lse)
     return lse == -INFINITY ? -INFINITY : lse * -1.4426950408889634f;
 }
 
-// (d0, d1) = (a0 * b + c0, a1 * b + c1), packed
-__device__ __forceinline__ void ffma2_s(float& d0, float& d1, float a0, float a1, float b, float c0, float c1)
-{
-    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
-        "mov.b64 ra, {%2, %3};\n\t"
-        "mov.b64 rb, {%4, %4};\n\t"
-        "mov.b64 rc, {%5, %6};\n\t"
-        "fma.rn.f32x2 rd, ra, rb, rc;\n\t"
-        "mov.b64 {%0, %1}, rd;\n\t}"
-        : "=f"(d0), "=f"(d1)
-        : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
-}
-
 // A query item's count, clamped as the forward clamps it.
 template <bool KV>
 __device__ __forceinline__ int item_count(const AttnBwdArgs& a, int item)
@@ -500,25 +487,21 @@ __device__ __forceinline__ void run_side(const CUtensorMap* tm_x0, const CUtenso
                         l4 = *reinterpret_cast<const float4*>(&x.info[e][0][32 * g + c]);
                         d4 = *reinterpret_cast<const float4*>(&x.info[e][1][32 * g + c]);
                     }
-                    float e0, e1, e2, e3;
-                    ffma2_s(e0, e1, sv[c], sv[c + 1], a.scale_log2, l4.x, l4.y);
-                    ffma2_s(e2, e3, sv[c + 2], sv[c + 3], a.scale_log2, l4.z, l4.w);
-                    e0 = fast_exp2(e0);
-                    e1 = fast_exp2(e1);
-                    e2 = fast_exp2(e2);
-                    e3 = fast_exp2(e3);
+                    const float2 sc = make_float2(a.scale_log2, a.scale_log2);
+                    float2 e0 = __ffma2_rn(make_float2(sv[c], sv[c + 1]), sc, make_float2(l4.x, l4.y));
+                    float2 e1 = __ffma2_rn(make_float2(sv[c + 2], sv[c + 3]), sc, make_float2(l4.z, l4.w));
+                    e0 = make_float2(fast_exp2(e0.x), fast_exp2(e0.y));
+                    e1 = make_float2(fast_exp2(e1.x), fast_exp2(e1.y));
                     if constexpr (KV) {
-                        pk[c / 2] = pack_bf16x2(e0, e1);
-                        pk[c / 2 + 1] = pack_bf16x2(e2, e3);
+                        pk[c / 2] = pack_bf16x2(e0.x, e0.y);
+                        pk[c / 2 + 1] = pack_bf16x2(e1.x, e1.y);
                     }
-                    fadd2_acc(dp[c], dp[c + 1], d4.x, d4.y);
-                    fadd2_acc(dp[c + 2], dp[c + 3], d4.z, d4.w);
-                    fmul2(e0, e1, dp[c], dp[c + 1]);
-                    fmul2(e2, e3, dp[c + 2], dp[c + 3]);
+                    e0 = __fmul2_rn(e0, __fadd2_rn(make_float2(dp[c], dp[c + 1]), make_float2(d4.x, d4.y)));
+                    e1 = __fmul2_rn(e1, __fadd2_rn(make_float2(dp[c + 2], dp[c + 3]), make_float2(d4.z, d4.w)));
                     // a streamed key that is not there contributes nothing, whatever its P came out as
                     // (a streamed query that is not there has P = 0)
-                    dk[c / 2] = KV || valid ? pack_bf16x2(e0, e1) : 0u;
-                    dk[c / 2 + 1] = KV || valid ? pack_bf16x2(e2, e3) : 0u;
+                    dk[c / 2] = KV || valid ? pack_bf16x2(e0.x, e0.y) : 0u;
+                    dk[c / 2 + 1] = KV || valid ? pack_bf16x2(e1.x, e1.y) : 0u;
                 }
                 if (!(ok = mbar_wait(&m.p_empty[t % L::PBUFS], ((t / L::PBUFS) & 1) ^ 1, abort_flag, a.err, 0x64))) break;
 #pragma unroll
