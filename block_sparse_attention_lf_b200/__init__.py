@@ -25,6 +25,21 @@ frames (keep the pooled keys of past frames between calls),
 ``lf_select_blocks_1d`` gives the single-granularity lists of the ablation, and
 ``lf_cag_budget`` / ``lf_blocks_for_sparsity`` turn a sparsity target into
 per-chunk block counts.
+
+Fine-tuning a block under sparsity (the call's gradient, and what stands on both sides
+of the call)::
+
+    lf_norm_gate(NormGateShape.make(rows, dim, F, torch.float32, torch.bfloat16, pre="layer", post="none"),
+                 x, y, r, h, gate=..., scale=..., shift=...)       # residual stream r, block input h
+    call = HSACall(shape, chunk_index, topk_frames, topk_blocks, train=True)
+    call.load(RopePlan.make(D, axis_dims=(44, 42, 42)), qkv, positions, q, k, v)
+    out = call(q, k, v)                                            # also keeps lse and out_lo
+    call.backward(q, k, v, dout, dq, dk, dv)                       # over the lists of the forward
+    call.load_bwd(plan, dq, dk, dv, positions, dqkv)
+    lf_norm_gate_bwd(..., x, y, dr, dh, dx, dy, grads, workspace)
+
+Nothing here records an autograd graph; a training program calls the gradients where its
+own does.
 """
 from __future__ import annotations
 

@@ -861,7 +861,6 @@ lf_status lf_norm_gate(const lf_norm_gate_shape* shape, const lf_norm_gate_vecto
     a.y = y;
     a.r = r;
     a.h = h;
-    if ((st = error_word(&a.err)) != LF_OK) return st;
     return launch_status(lf::launch_norm_fwd(a, shape->x_dtype, shape->y_dtype, static_cast<cudaStream_t>(stream)));
 }
 
@@ -910,7 +909,6 @@ lf_status lf_norm_gate_bwd(const lf_norm_gate_shape* shape, const lf_norm_gate_v
     a.dh = dh;
     a.dx = dx;
     a.dy = dy;
-    if ((st = error_word(&a.err)) != LF_OK) return st;
     a.n_cta = lf::norm_bwd_ctas(shape->rows);
     a.part_w = static_cast<float*>(workspace);
     a.part = a.part_w + static_cast<long long>(a.n_cta) * 4 * ((shape->dim + 7) / 8 * 8);

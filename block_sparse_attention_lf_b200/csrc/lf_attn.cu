@@ -215,7 +215,9 @@ __device__ __forceinline__ void tmem_ld128_nowait(uint32_t taddr, float (&v)[128
     }
 }
 
-template <int D, bool IL, bool F8>
+// TRAIN: lse and, where it is asked for, out_lo are written too; a variant of its own, since the
+// plain call's time at layer480p rose from 323.5 to 334.7 us when it only tested for them.
+template <int D, bool IL, bool F8, bool TRAIN>
 __global__ void __launch_bounds__(ATTN_THREADS, 1)
 attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q_rem,
             const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_k_rem,
@@ -556,7 +558,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const float m_new = need ? ms : m_run;
             const float alpha = need ? fast_exp2(m_run - m_new) : 1.f;  // 0 when m_run = -inf
             l_run *= alpha;
-            if constexpr (!F8) lt_run *= alpha;
+            if constexpr (TRAIN) lt_run *= alpha;
             m_run = m_new;
             // 2. Probabilities (registers), then wait until the PV of this warpgroup's
             // previous step has read its P buffer and finished accumulating into its O^T.
@@ -573,7 +575,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 pk[c >> 1] = pack_bf16x2(p0, p1);
             }
             l_run += la + lb;
-            if (!F8 && a.out_lo) {
+            if (TRAIN && a.out_lo) {
                 float ta = 0.f, tb = 0.f;
 #pragma unroll
                 for (int c = 0; c < 64; ++c) fadd2_acc(ta, tb, __uint_as_float(pk[c] << 16), __uint_as_float(pk[c] & 0xFFFF0000u));
@@ -624,7 +626,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 
         // ------------------------------------------------------------ epilogue
         const float l_row = l_run + __shfl_xor_sync(0xffffffffu, l_run, 16);
-        if constexpr (!F8) {
+        if constexpr (TRAIN) {
             const float lt_row = lt_run + __shfl_xor_sync(0xffffffffu, lt_run, 16);
             if (hh == 0) x.ltsum[g][qr] = lt_row;
         }
@@ -658,14 +660,14 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             x.wgt[0][cc] = f0 * inv;
             x.wgt[1][cc] = f1 * inv;
             // training: the row under the rounded weights, which sum to dent, is the row times den / dent
-            const float dent = F8 ? 0.f : x.ltsum[0][cc] * f0 + x.ltsum[1][cc] * f1;
-            if (!F8 && a.out_lo) x.renorm[cc] = dent > 0.f ? den / dent : 1.f;
+            const float dent = !TRAIN ? 0.f : x.ltsum[0][cc] * f0 + x.ltsum[1][cc] * f1;
+            if (TRAIN && a.out_lo) x.renorm[cc] = dent > 0.f ? den / dent : 1.f;
             if (slot >= 0) {
                 float* ml = a.part_ml + (static_cast<long long>(slot) * 64 + cc) * 2;
                 ml[0] = den > 0.f ? mx : -INFINITY;
                 ml[1] = den > 0.f ? den : 0.f;
-                if (!F8 && a.out_lo) a.part_lt[static_cast<long long>(slot) * 64 + cc] = den > 0.f ? dent : 0.f;
-            } else if (!F8 && a.lse && cc < q_rows) {
+                if (TRAIN && a.out_lo) a.part_lt[static_cast<long long>(slot) * 64 + cc] = den > 0.f ? dent : 0.f;
+            } else if (TRAIN && cc < q_rows) {
                 // natural log from the base-2 maximum and the fp32 denominator
                 a.lse[q_row0 + cc] = den == 0.f ? -INFINITY : (mx + log2f(den)) * 0.69314718055994531f;
             }
@@ -694,7 +696,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     const float o = (w0 != 0.f ? o0[c] * w0 : 0.f) + (w1 != 0.f ? o1[c] * w1 : 0.f);
                     const __nv_bfloat16 hi = __float2bfloat16_rn(o);
                     ostage[cc * D + t] = hi;
-                    if (!F8 && a.out_lo) lstage[cc * D + t] = __float2bfloat16_rn(o * x.renorm[cc] - __bfloat162float(hi));
+                    if (TRAIN && a.out_lo) lstage[cc * D + t] = __float2bfloat16_rn(o * x.renorm[cc] - __bfloat162float(hi));
                 }
             }
             named_bar_sync(3, 256);
@@ -704,7 +706,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 const int c8 = idx - qq * (D / 8);
                 const long long at = (static_cast<long long>(q_row0) + qq) * D + c8 * 8;
                 *reinterpret_cast<uint4*>(a.out + at) = *reinterpret_cast<const uint4*>(ostage + qq * D + c8 * 8);
-                if (!F8 && a.out_lo) *reinterpret_cast<uint4*>(a.out_lo + at) = *reinterpret_cast<const uint4*>(lstage + qq * D + c8 * 8);
+                if (TRAIN && a.out_lo) *reinterpret_cast<uint4*>(a.out_lo + at) = *reinterpret_cast<const uint4*>(lstage + qq * D + c8 * 8);
             }
         }
     }
@@ -724,7 +726,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 // eight rows per CTA; lane l holds head-dim elements [V l, V l + V). Lane i
 // computes the weight of piece p0 + i, which a shuffle hands to the whole warp,
 // so the loads of consecutive pieces are independent.
-template <int D>
+template <int D, bool TRAIN>
 __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnArgs a)
 {
     constexpr int V = D / 32;  // 4 (head_dim 128) or 2 (head_dim 64)
@@ -759,7 +761,7 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnArgs a)
             const float mp = ml[static_cast<long long>(p0 + lane) * 128];
             if (mp != -INFINITY) {
                 wl = fast_exp2(mp - M) * ml[static_cast<long long>(p0 + lane) * 128 + 1];
-                if (a.out_lo) dent += fast_exp2(mp - M) * a.part_lt[(s0 + p0 + lane) * 64 + qq];
+                if (TRAIN && a.out_lo) dent += fast_exp2(mp - M) * a.part_lt[(s0 + p0 + lane) * 64 + qq];
             }
         }
         den += wl;
@@ -784,11 +786,11 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnArgs a)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         den += __shfl_xor_sync(0xffffffffu, den, o);
-        dent += __shfl_xor_sync(0xffffffffu, dent, o);
+        if constexpr (TRAIN) dent += __shfl_xor_sync(0xffffffffu, dent, o);
     }
     const float renorm = dent > 0.f ? den / dent : 1.f;  // as in the attention kernel's epilogue
     const float inv = den > 0.f ? 1.f / den : 0.f;
-    if (a.lse && lane == 0) a.lse[q_row] = den == 0.f ? -INFINITY : (M + log2f(den)) * 0.69314718055994531f;
+    if (TRAIN && lane == 0) a.lse[q_row] = den == 0.f ? -INFINITY : (M + log2f(den)) * 0.69314718055994531f;
     float rest[V];  // the row under the rounded weights, less out
     uint32_t hi[V / 2];
 #pragma unroll
@@ -802,14 +804,14 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnArgs a)
     const long long at = q_row * D + V * lane;
     if constexpr (V == 4) {
         *reinterpret_cast<uint2*>(a.out + at) = make_uint2(hi[0], hi[1]);
-        if (a.out_lo) *reinterpret_cast<uint2*>(a.out_lo + at) = make_uint2(pack_bf16x2(rest[0], rest[1]), pack_bf16x2(rest[2], rest[3]));
+        if (TRAIN && a.out_lo) *reinterpret_cast<uint2*>(a.out_lo + at) = make_uint2(pack_bf16x2(rest[0], rest[1]), pack_bf16x2(rest[2], rest[3]));
     } else {
         *reinterpret_cast<uint32_t*>(a.out + at) = hi[0];
-        if (a.out_lo) *reinterpret_cast<uint32_t*>(a.out_lo + at) = pack_bf16x2(rest[0], rest[1]);
+        if (TRAIN && a.out_lo) *reinterpret_cast<uint32_t*>(a.out_lo + at) = pack_bf16x2(rest[0], rest[1]);
     }
 }
 
-template <int D, bool IL, bool F8>
+template <int D, bool IL, bool F8, bool TRAIN = false>
 cudaError_t launch_attn_t(const AttnMaps& m, const AttnArgs& a, cudaStream_t s)
 {
     constexpr uint32_t smem = attn_smem_bytes<D, IL, F8>();
@@ -819,7 +821,7 @@ cudaError_t launch_attn_t(const AttnMaps& m, const AttnArgs& a, cudaStream_t s)
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (configured_device != dev) {
-        e = cudaFuncSetAttribute(attn_kernel<D, IL, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        e = cudaFuncSetAttribute(attn_kernel<D, IL, F8, TRAIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
         configured_device = dev;
     }
@@ -838,7 +840,7 @@ cudaError_t launch_attn_t(const AttnMaps& m, const AttnArgs& a, cudaStream_t s)
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, attn_kernel<D, IL, F8>, m.q, m.q_rem, m.k, m.k_rem, m.v, m.v_rem, a);
+        e = cudaLaunchKernelEx(&cfg, attn_kernel<D, IL, F8, TRAIN>, m.q, m.q_rem, m.k, m.k_rem, m.v, m.v_rem, a);
     }
     if (e != cudaSuccess || tail == 0) return e;
     cudaLaunchConfig_t cfg = {};
@@ -851,7 +853,7 @@ cudaError_t launch_attn_t(const AttnMaps& m, const AttnArgs& a, cudaStream_t s)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_merge_kernel<D>, a);
+    return cudaLaunchKernelEx(&cfg, attn_merge_kernel<D, TRAIN>, a);
 }
 
 }  // namespace
@@ -859,6 +861,11 @@ cudaError_t launch_attn_t(const AttnMaps& m, const AttnArgs& a, cudaStream_t s)
 cudaError_t launch_attn(const AttnMaps& m, const AttnArgs& a, int D, bool interleaved, cudaStream_t s)
 {
     if (a.n_units <= 0) return cudaSuccess;
+    if (a.lse) {
+        if (D == 128)
+            return interleaved ? launch_attn_t<128, true, false, true>(m, a, s) : launch_attn_t<128, false, false, true>(m, a, s);
+        return launch_attn_t<64, false, false, true>(m, a, s);
+    }
     if (D == 128)
         return interleaved ? launch_attn_t<128, true, false>(m, a, s) : launch_attn_t<128, false, false>(m, a, s);
     return launch_attn_t<64, false, false>(m, a, s);

@@ -25,8 +25,9 @@
 //
 // CTAs are persistent and take consecutive rows, so the vectors of a group stay in
 // registers, folded to what a row needs (gate w2, gate b2, (1 + scale) w1, b1 (1 + scale) +
-// shift), and rows arrive ahead through a ring of bulk copies: a row has several dependent
-// sums, and only loads that are many rows ahead keep the memory busy meanwhile. Rows that do
+// shift), and rows are copied ahead into a ring in shared memory: a row has several dependent
+// sums, and only loads that are rows ahead keep the memory busy meanwhile. Each thread copies
+// what it will read itself, so the ring needs no barrier. Rows that do
 // not start on 16-byte boundaries (dim not a multiple of 8), and rows too long for a ring,
 // are loaded directly.
 //
@@ -39,9 +40,10 @@ namespace lf {
 namespace {
 
 // A row's sums cost a warp the same whatever it holds of the row, and the vectors have to stay in
-// registers (read per row from L1 they took 151-250 us where this takes 104). So a thread holds as
+// registers (read per row from L1 they took 151-250 us where this takes 93). So a thread holds as
 // many groups of eight as leave three CTAs of 128 threads an SM: at 32760 rows of 1536 bf16, 24
-// elements in 64 threads 104 us, 8 in 192 threads 138 us. Where there are few rows latency counts, and
+// elements in 64 threads take 93 us (302 MB, 3.2 TB/s), 8 in 192 threads 138 us; what is left is the
+// row's two dependent sums and the issue of its arithmetic by few warps, not the memory. Where there are few rows latency counts, and
 // more threads of one group each share a row (one row of 1536: 4.2 against 6.7 us).
 // WIDE: a CTA of up to 512 threads for one row.
 constexpr int FWD_THREADS = 128;

@@ -26,7 +26,6 @@ struct NormArgs {
     float* part;    // gradient: [slot][4][dim8] partial column sums; slot = CTA + group
     float* part_w;  // [CTA][4][dim8]: the same times 1 + scale or the gate, for the weights' gradients
     bool weights;   // any of those is wanted
-    int* err;       // device error word (an expired bounded wait)
     long long rows, per_group;
     int dim, pre, post;
     float eps, alpha;

@@ -1,5 +1,5 @@
 // lf_norm_rows.cuh -- what the forward and gradient kernels of the gated residual norms share:
-// rows of 8-element groups in registers, team sums, the ring of bulk-copied rows, launch plans.
+// rows of 8-element groups in registers, team sums, the ring of rows copied ahead, launch plans.
 #pragma once
 
 #include "lf_norm.h"

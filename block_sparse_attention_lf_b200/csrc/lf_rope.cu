@@ -14,7 +14,8 @@
 // unit (a 16-byte vector, or two half a head apart) once and uses them for every head
 // it takes, so the fp64 work is spread over heads * tensors vectors.
 //
-// Memory-bound: each element is read and written once. A unit is the widest vector (16, 8, 4 or
+// Memory-bound: each element is read and written once (32760 tokens of 12 x 128 bf16, 201 MB:
+// 34.5 us, 5.8 TB/s). A unit is the widest vector (16, 8, 4 or
 // 2 bytes) that pointers, strides and spans allow; a thread asks for several heads' units before
 // it forms the angles, which take longer than a head's arithmetic, and for the next heads' before
 // it stores these. Frequencies are staged in shared memory: lanes need different ones, which the

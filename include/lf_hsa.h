@@ -64,7 +64,9 @@
  *   lf_block_sparse_attn_static uses a fixed scratch array compiled into the
  *   library instead. The library never allocates,
  *   frees or synchronises; each call only enqueues kernels on `stream`
- *   (a cudaStream_t; NULL = the legacy default stream) and returns.
+ *   (a cudaStream_t; NULL = the legacy default stream) and returns. The first
+ *   call of an entry point on a device loads its kernels and belongs before a
+ *   stream capture; later calls may be captured.
  * - Device pointers must be 16-byte aligned (the attention kernel reads them
  *   with TMA). Arguments are validated before anything is launched; a failed
  *   validation launches nothing.
