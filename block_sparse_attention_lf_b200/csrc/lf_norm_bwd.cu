@@ -6,8 +6,9 @@ namespace lf {
 namespace {
 
 // One CTA an SM, so that few partial sums are written: 384 threads that hold two groups of eight
-// (32760 rows of 1536 bf16, 604 MB: 208 us, 2.9 TB/s; one group in 192 threads 284, three in 64
-// threads 266). The bound is a row's chain of four dependent sums and the issue of its arithmetic by
+// (32760 rows of 1536 bf16, 604 MB: 202 us, 3.0 TB/s; one group in 192 threads 284, three in 64
+// threads 266). What the row's first halves need is read before the sums that precede its use, as far
+// as registers last (208 without; with every read so, 337: it spills). The bound is a row's chain of four dependent sums and the issue of its arithmetic by
 // twelve warps; more warps would leave the column sums no registers. WIDE:
 // longer rows take up to 512 threads, of two groups to 8192 and of four above.
 template <bool WIDE> constexpr int BWD_REGS = WIDE ? 128 : 168;
@@ -75,16 +76,16 @@ __global__ void __maxnreg__(BWD_REGS<WIDE>) norm_bwd_kernel(const NormArgs a, in
         __syncthreads();
         for (int col = threadIdx.x * 8; col < dim8; col += blockDim.x * 8) {
             const Vec8 v = load_param(a.v.gate ? a.v.gate + g : nullptr, col, dim, p.al, 1.f);
-            vec_store(vecs, col, mul(load_param(a.v.post_w, col, dim, p.al, 1.f), v));
-            vec_store(vecs + dim8, col, mul(load_param(a.v.pre_w, col, dim, p.al, 1.f),
-                                            add(load_param(a.v.scale ? a.v.scale + g : nullptr, col, dim, p.al, 0.f), 1.f)));
-            if (BIAS) vec_store(vecs + 2 * dim8, col, mul(load_param(a.v.post_b, col, dim, p.al, 0.f), v));
+            split_store(vecs, col, dim8, mul(load_param(a.v.post_w, col, dim, p.al, 1.f), v));
+            split_store(vecs + dim8, col, dim8, mul(load_param(a.v.pre_w, col, dim, p.al, 1.f),
+                                                    add(load_param(a.v.scale ? a.v.scale + g : nullptr, col, dim, p.al, 0.f), 1.f)));
+            if (BIAS) split_store(vecs + 2 * dim8, col, dim8, mul(load_param(a.v.post_b, col, dim, p.al, 0.f), v));
         }
         __syncthreads();
         // a vector of the group at the thread's k-th eight columns
         auto vec = [&](int which, int k) {
             const int col = p.col0 + k * p.stride;
-            return FULL || col < dim8 ? vec_load(vecs + which * dim8, col) : fill8(0.f);
+            return FULL || col < dim8 ? split_load(vecs + which * dim8, col, dim8) : fill8(0.f);
         };
         Vec8 A[4][NV];
 #pragma unroll
@@ -96,6 +97,11 @@ __global__ void __maxnreg__(BWD_REGS<WIDE>) norm_bwd_kernel(const NormArgs a, in
             Vec8 m[NV], n[NV], d[NV];
             float rs1 = 1.f, rs2 = 1.f;
             // forward again: m = post(y), n = pre(r)
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                n[k] = x.get(st, k, p);
+                n[k] = BIAS ? fma(n[k], a.alpha, vec(2, k)) : mul(n[k], a.alpha);
+            }
             if (y.on) {
 #pragma unroll
                 for (int k = 0; k < NV; ++k) m[k] = y.get(st, k, p);
@@ -103,18 +109,19 @@ __global__ void __maxnreg__(BWD_REGS<WIDE>) norm_bwd_kernel(const NormArgs a, in
             }
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const Vec8 v = x.get(st, k, p);
-                n[k] = BIAS ? fma(v, a.alpha, vec(2, k)) : mul(v, a.alpha);
                 if (y.on) n[k] = fma(vec(0, k), m[k], n[k]);
             }
             float q1 = 0.f, q2 = 0.f;
             if (dh.on) {
-                rs1 = normalise<NV, FULL>(team, n, a.pre, inv, p, a.eps);
-                float2 u = make_float2(0.f, 0.f), w = u;
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
                     d[k] = dh.get(st, k, p);
                     A[0][k] = add(A[0][k], d[k]);
+                }
+                rs1 = normalise<NV, FULL>(team, n, a.pre, inv, p, a.eps);
+                float2 u = make_float2(0.f, 0.f), w = u;
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
                     A[1][k] = fma(d[k], n[k], A[1][k]);
                     d[k] = mul(d[k], vec(1, k));
                     acc(u, d[k]);
@@ -276,7 +283,7 @@ template <typename TX, typename TY, int NV, bool WIDE>
 cudaError_t launch_nv(const NormArgs& a, cudaStream_t s)
 {
     const size_t elem = sizeof(TX) * (a.dr ? 2 : 1) + sizeof(TY) * ((a.y ? 1 : 0) + (a.dh ? 1 : 0));
-    const NormPlan p = plan_of(a.dim, NV, elem, WIDE ? 128 : BWD_THREADS, 1, true);
+    const NormPlan p = plan_of(a.dim, NV, elem, WIDE ? 128 : BWD_THREADS, 1, 2, 1);  // 3 vectors, teams - 1 folded sums
     const bool bias = a.v.post_b || a.dpost_b;
     cudaError_t e;
     if (p.full)

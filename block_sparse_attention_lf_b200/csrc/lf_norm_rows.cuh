@@ -158,6 +158,25 @@ __device__ __forceinline__ Vec8 load_param(const float* p, int col, int dim, boo
     return p ? unpack8(load_raw(p, col, dim, al)) : head8(fill8(other), dim - col);
 }
 
+// A vector of the CTA's in shared memory: the first fours of all eights, then the second fours, so
+// that neighbouring threads meet different banks.
+__device__ __forceinline__ void split_store(float* p, int col, int dim8, const Vec8& x)
+{
+    *reinterpret_cast<float4*>(p + col / 2) = make_float4(x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y);
+    *reinterpret_cast<float4*>(p + dim8 / 2 + col / 2) = make_float4(x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y);
+}
+
+__device__ __forceinline__ Vec8 split_load(const float* p, int col, int dim8)
+{
+    const float4 a = *reinterpret_cast<const float4*>(p + col / 2), b = *reinterpret_cast<const float4*>(p + dim8 / 2 + col / 2);
+    Vec8 o;
+    o.v[0] = make_float2(a.x, a.y);
+    o.v[1] = make_float2(a.z, a.w);
+    o.v[2] = make_float2(b.x, b.y);
+    o.v[3] = make_float2(b.z, b.w);
+    return o;
+}
+
 constexpr int MAX_TEAMS = 12, MAX_STAGES = 4;
 
 // Row sums over a team of whole warps, in a fixed order. Consecutive calls alternate between two
@@ -175,8 +194,11 @@ struct Team {
     __device__ __forceinline__ float gather(int which)
     {
         const float4* f = reinterpret_cast<const float4*>(red[phase][which]);
-        const float4 u = f[0], v = f[1];
-        float s = ((u.x + u.y) + (u.z + u.w)) + ((v.x + v.y) + (v.z + v.w));
+        const float4 u = f[0];
+        float s = (u.x + u.y) + (u.z + u.w);
+        if (warps <= 4) return s;
+        const float4 v = f[1];
+        s += (v.x + v.y) + (v.z + v.w);
         if (warps > 8) {
             const float4 w = f[2], x = f[3];
             s += ((w.x + w.y) + (w.z + w.w)) + ((x.x + x.y) + (x.z + x.w));
@@ -389,8 +411,9 @@ struct NormPlan {
     size_t smem;
 };
 
-// nv groups of a thread; elem_bytes: of the streams read, together.
-NormPlan plan_of(int dim, int nv, size_t elem_bytes, int cta_threads, int ctas, bool gradient)
+// nv groups of a thread; elem_bytes: of the streams read, together; vectors of a row's length that the
+// CTA, and each of its teams, keeps in shared memory beside the rings.
+NormPlan plan_of(int dim, int nv, size_t elem_bytes, int cta_threads, int ctas, int vectors, int team_vectors)
 {
     NormPlan p;
     const int vecs = (dim + 7) / 8;
@@ -398,7 +421,7 @@ NormPlan plan_of(int dim, int nv, size_t elem_bytes, int cta_threads, int ctas, 
     p.threads = ((vecs + nv - 1) / nv + 31) / 32 * 32;
     p.wide = p.threads > cta_threads;
     p.teams = p.wide ? 1 : std::min(MAX_TEAMS, cta_threads / p.threads);
-    const size_t extra = gradient ? static_cast<size_t>(p.teams + 2) * vecs * 8 * sizeof(float) : 0;  // vectors, folded sums
+    const size_t extra = static_cast<size_t>(vectors + team_vectors * p.teams) * vecs * 8 * sizeof(float);
     const size_t room = (220u * 1024u) / (p.wide ? 1 : ctas) - 4096 - extra;
     const size_t stage = elem_bytes * p.threads * nv * 8;  // a team's row
     const int fit = static_cast<int>(std::min<size_t>(room / (stage * p.teams), MAX_STAGES));

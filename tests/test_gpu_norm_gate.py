@@ -29,6 +29,14 @@ CASES = [
     (6, 12289, 4, "fp32", "bf16", "layer", "layer", "gate post_w"),
     (2000, 256, 1, "bf16", "bf16", "layer", "none", "gate scale shift"),  # a group a row
     (1111, 320, 600, "fp32", "fp32", "rms", "rms", " ".join(NAMES)),      # groups cross the CTAs' rows
+    # more rows than four an SM: a CTA's teams share a group's vectors, or keep their own for short groups
+    (700, 1536, 130, "bf16", "bf16", "layer", "layer", " ".join(NAMES)),
+    (1300, 512, 64, "bf16", "bf16", "rms", "rms", " ".join(NAMES)),       # a CTA meets two groups
+    (650, 2048, 100, "fp32", "fp32", "rms", "layer", " ".join(NAMES)),    # no room for a ring
+    (601, 1000, 64, "fp32", "bf16", "layer", "rms", "gate shift pre_w"),  # threads past the row's end
+    (777, 1333, 300, "fp16", "fp16", "layer", "layer", " ".join(NAMES)),  # odd
+    (900, 1992, 3, "fp32", "bf16", "rms", "rms", "gate scale shift"),
+    (640, 1024, 63, "bf16", "bf16", "layer", "none", "scale shift"),
 ]
 
 
