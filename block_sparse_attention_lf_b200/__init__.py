@@ -190,7 +190,7 @@ class NormGateShape(ctypes.Structure):
 
     @property
     def groups(self) -> int:
-        return -(-self.rows // self.rows_per_group)
+        return -(-self.rows // max(self.rows_per_group, 1))  # below 1: refused by the library
 
 
 _NORM_VECTORS = ("gate", "scale", "shift", "pre_w", "pre_b", "post_w", "post_b")
@@ -776,12 +776,13 @@ class HSACall:
                 tail, pieces = 0, 0
         else:
             tail, pieces = 0, 0
-        ws_bytes = tail * pieces * 64 * (D + 2) * 4
+        ws_bytes = tail * pieces * 64 * (D + (3 if train else 2)) * 4  # a piece slot; training keeps one sum more
         self.workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device) if ws_bytes else None
         self.split = (tail, pieces) if ws_bytes else (0, 0)
         self.lse = torch.empty(s.batch, s.heads, s.Lq, dtype=f32, device=device) if train else None
         self.out_lo = torch.empty_like(self.buf.out) if train else None
         self.bwd_workspace = torch.empty(lf_attn_bwd_workspace(s), dtype=torch.uint8, device=device) if train else None
+        self.attended = False
         # kernels enqueued per call: pool, selection (both levels), attention (+ the merge of a split)
         self.launches_per_call = 3 + (1 if ws_bytes else 0)
 
@@ -811,14 +812,15 @@ class HSACall:
 
     def backward(self, q, k, v, dout, dq, dk, dv, stream=None):
         """Gradients of the last call's output in q, k and v (``train=True``; the selected blocks are constants)."""
-        if self.lse is None:
-            raise ValueError("HSACall.backward needs train=True")
+        if self.lse is None or not self.attended:
+            raise ValueError("HSACall.backward needs train=True and a call before it")
         b = self.buf
         lf_block_sparse_attn_bwd(self.shape, q, k, v, b.out, dout, self.lse, b.block_list, b.block_count, b.list_cap,
                                  self.softmax_scale, dq, dk, dv, self.bwd_workspace, stream, out_lo=self.out_lo)
 
     def attend(self, q, k, v, stream=None):
         b = self.buf
+        self.attended = True
         if self.lse is not None:
             lf_block_sparse_attn_lse(self.shape, q, k, v, b.block_list, b.block_count, b.list_cap,
                                      self.softmax_scale, b.out, self.lse, self.workspace, self.tail_pieces, stream,

@@ -439,8 +439,8 @@ LF_API lf_status lf_block_sparse_attn_fp8(const lf_hsa_shape* shape, const uint8
  *        With it a piece slot of the workspace takes 64 * (head_dim + 3) * 4 bytes.
  *   lse  [B,H,Lq] fp32: log sum_s exp(scale * <q_t, k_s>) over the row's listed
  *        tokens (natural log); -inf for a row whose list is empty.
- * out is bit-identical to lf_block_sparse_attn_ws. Two partial results over
- * disjoint lists combine through their lse.
+ * out is bit-identical to lf_block_sparse_attn_ws where the lists are split alike.
+ * Two partial results over disjoint lists combine through their lse.
  * Errors: those of lf_block_sparse_attn_ws; LF_ERR_NULL / LF_ERR_ALIGN for lse.
  */
 LF_API lf_status lf_block_sparse_attn_lse(const lf_hsa_shape* shape, const uint16_t* q, const uint16_t* k,

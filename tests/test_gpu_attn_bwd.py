@@ -298,3 +298,23 @@ def test_call_trains_and_loads():
     assert torch.equal(dqkv[:, :, 2].transpose(1, 2), dv[:, :, (NF - nc) * F:])
     with pytest.raises(ValueError):
         L.HSACall(shape, 2, 2, 1).backward(q, k, v, do, dq, dk, dv)
+
+
+def test_train_call_splits_as_the_plain_one():
+    """The last wave's lists are cut into as many pieces with the sums that training adds, so out keeps its bits."""
+    shape = L.LfShape.make(1, 1, 128, 320, 8, 1, 1, 2)
+    g = torch.Generator().manual_seed(43)
+    q = torch.randn(1, 1, 640, 128, generator=g).to(BF).cuda()
+    k, v = (torch.randn(1, 1, 8 * 320, 128, generator=g).to(BF).cuda() for _ in range(2))
+    plain, train = (L.HSACall(shape, 2, 2, 5, train=t) for t in (False, True))
+    tail, pieces = train.split
+    assert (tail, pieces) == plain.split and pieces >= 2
+    assert train.workspace.numel() == tail * pieces * 64 * (128 + 3) * 4
+    assert torch.equal(plain(q, k, v), train(q, k, v))
+
+
+def test_gradient_before_a_call_is_refused():
+    shape = L.LfShape.make(1, 1, 64, 64, 4, 1, 1, 1)
+    t = [torch.zeros(1, 1, n, 64, dtype=BF, device="cuda") for n in (64, 256, 256, 64, 64, 256, 256)]
+    with pytest.raises(ValueError):
+        L.HSACall(shape, 2, 1, 1, train=True).backward(*t)
