@@ -51,6 +51,7 @@
 // softmax - products. Tried and left: S' and dP' on barriers of their own, a third Xs tile for key
 // items in place of the second own block, dk before dv (each slower or within 20 us).
 #include "lf_attn_bwd.h"
+#include "lf_internal.h"
 #include "lf_device.cuh"
 
 #include <cuda_bf16.h>
@@ -629,6 +630,7 @@ attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // everything above overlaps the preparing kernel
     if (!x.abort) run_side<D, false>(&tm_q, &tm_dout, &tm_k, &tm_v, a, smem, x);
     __syncwarp();
     tc_fence_before();
@@ -662,6 +664,9 @@ template <int D>
 __global__ void __launch_bounds__(PREP_THREADS) attn_bwd_prep_kernel(const AttnBwdArgs a, int transposing)
 {
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // only now: the gradient's CTAs take all of an SM's tensor memory, which the forward has left
+    if (t == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (static_cast<int>(blockIdx.x) < transposing) {
         __shared__ uint32_t bits[TR_WORDS][TR_BLOCKS];
         if (blockIdx.x == 0 && t < 2) a.next_item[t] = 0;
@@ -749,11 +754,11 @@ cudaError_t launch_d(const AttnBwdMaps& m, const AttnBwdArgs& a, cudaStream_t s)
     const int transposing = (a.Nkv + TR_BLOCKS - 1) / TR_BLOCKS * a.BH;
     const long long rows = static_cast<long long>(a.BH) * a.Lq;
     const unsigned prep = static_cast<unsigned>(transposing + (rows + DELTA_ROWS - 1) / DELTA_ROWS);
-    attn_bwd_prep_kernel<D><<<prep, PREP_THREADS, 0, s>>>(a, transposing);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_dependent(attn_bwd_prep_kernel<D>, dim3(prep), PREP_THREADS, 0, s, a, transposing);
+    if (e != cudaSuccess) return e;
     const long long items = static_cast<long long>(a.BH) * (a.Rq + a.Nkv);
-    attn_bwd_kernel<D><<<static_cast<unsigned>(items < sm ? items : sm), BWD_THREADS, smem, s>>>(m.q, m.dout, m.k, m.v, a);
-    return cudaGetLastError();
+    return launch_dependent(attn_bwd_kernel<D>, dim3(static_cast<unsigned>(items < sm ? items : sm)), BWD_THREADS, smem, s,
+                            m.q, m.dout, m.k, m.v, a);
 }
 
 }  // namespace

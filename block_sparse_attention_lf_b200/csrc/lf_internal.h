@@ -105,6 +105,24 @@ struct AttnMaps {
     CUtensorMap q, q_rem, k, k_rem, v, v_rem;
 };
 
+// Launches a kernel as a programmatic dependent of the one before it in the stream: it may be
+// scheduled while that one finishes, and waits for it (griddepcontrol.wait) before reading memory.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, const Args&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 cudaError_t launch_pool(const PoolArgs& a, cudaStream_t s);
 cudaError_t launch_select_frames(const SelectFramesArgs& a, cudaStream_t s);
 cudaError_t launch_select_blocks(const SelectBlocksArgs& a, cudaStream_t s);

@@ -1,6 +1,7 @@
 // lf_norm_bwd.cu -- gradients of the gated residual norms (formulas and the rows' way through a
 // team: lf_norm.cu).
 #include "lf_norm_rows.cuh"
+#include "lf_internal.h"
 
 namespace lf {
 namespace {
@@ -40,6 +41,7 @@ __global__ void __maxnreg__(BWD_REGS<WIDE>) norm_bwd_kernel(const NormArgs a, in
 {
     __shared__ __align__(16) float red[MAX_TEAMS][2][2][16];
     extern __shared__ __align__(16) uint8_t smem[];  // the rings, then [3][dim8] vectors and [teams - 1][dim8] sums
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the finish, which waits
     Team team = make_team(red, team_threads);
     const int teams = blockDim.x / team_threads;
     const int ti = threadIdx.x / team_threads, tt = threadIdx.x - ti * team_threads;
@@ -214,6 +216,7 @@ __global__ void __launch_bounds__(FIN_COLS * FIN_ROWS) norm_bwd_finish_kernel(co
     const int col = blockIdx.x * FIN_COLS + c;
     const int dim8 = (a.dim + 7) & ~7;
     const long long batches = (groups + FIN_GROUPS - 1) / FIN_GROUPS;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     for (long long batch = blockIdx.y; batch < batches + (a.weights ? 1 : 0); batch += gridDim.y) {
         const bool all = batch == batches;
         const int rows = all ? FIN_ROWS : FIN_ROWS / FIN_GROUPS, first = j % rows;
@@ -293,9 +296,8 @@ cudaError_t launch_nv(const NormArgs& a, cudaStream_t s)
     if (e != cudaSuccess || (!a.dgate && !a.dscale && !a.dshift && !a.weights)) return e;
     const long long groups = (a.rows + a.per_group - 1) / a.per_group;
     const long long items = (groups + FIN_GROUPS - 1) / FIN_GROUPS + (a.weights ? 1 : 0);
-    norm_bwd_finish_kernel<<<dim3((a.dim + FIN_COLS - 1) / FIN_COLS, static_cast<unsigned>(std::min<long long>(items, 65535))),
-                             FIN_COLS * FIN_ROWS, 0, s>>>(a, groups);
-    return cudaGetLastError();
+    const dim3 grid((a.dim + FIN_COLS - 1) / FIN_COLS, static_cast<unsigned>(std::min<long long>(items, 65535)));
+    return launch_dependent(norm_bwd_finish_kernel, grid, FIN_COLS * FIN_ROWS, 0, s, a, groups);
 }
 
 template <typename TX, typename TY>
