@@ -24,12 +24,11 @@
 // roundings to fewer bits are the stores of r, h, dx and dy.
 //
 // CTAs are persistent and take consecutive rows, so the vectors of a group stay in
-// registers or shared memory, folded to what a row needs (gate w2, gate b2, (1 + scale) w1, b1 (1 + scale) +
-// shift), and rows are copied ahead into a ring in shared memory: a row has several dependent
-// sums, and only loads that are rows ahead keep the memory busy meanwhile. Each thread copies
-// what it will read itself, so the ring needs no barrier. Rows that do
-// not start on 16-byte boundaries (dim not a multiple of 8), and rows too long for a ring,
-// are loaded directly.
+// registers or shared memory, folded to what a row needs (gate w2, gate b2, (1 + scale) w1,
+// b1 (1 + scale) + shift), and rows are copied ahead into a ring in shared memory: a row has several
+// dependent sums, and only loads that are rows ahead keep the memory busy meanwhile. Each thread
+// copies what it will read itself, so the ring needs no barrier. Rows that do not start on 16-byte
+// boundaries (dim not a multiple of 8), and rows too long for a ring, are loaded directly.
 //
 // The gradient kernel keeps its column sums in registers: a CTA writes one partial row per
 // group it meets (slot = CTA + group, so no two coincide) and one of its weights' sums, and a
@@ -41,16 +40,17 @@ namespace {
 
 // Two kernels, and rows too long for the first. The group kernel: one CTA of 512 threads an SM, the
 // folded vectors of a group in shared memory for all its teams. A row's sums cost a warp the same
-// whatever it holds of the row, so a thread holds up to 32 elements and a team is 64 threads or few
-// more (fp32 rows of 2048, whose ring does not fit, are loaded directly: 113 us for 16384 rows; fewer
-// teams with a ring 126). At 32760 rows of 1536 bf16 it takes 80 us (302 MB, 3.8 TB/s); what is left is the row's two
-// dependent sums and the issue of its arithmetic by 16 warps, not the memory. Vectors in registers took
-// 94, read per row from L1 151-250; 768 threads of 80 registers 99 (they spill), every shared read
-// before the sum that it follows 93 (likewise).
-// The register kernel: every team goes its own way, the folded vectors in its registers, for
-// groups too short to stop the CTA at (1024 elements a row, groups of 1 and 16 rows: 171 and 69 against
-// 703 and 94 us; 1536, groups of 64: 92 against 87, of 256: 87 against 77), and for few rows, where latency counts and more
-// threads of one group of eight each share a row (one row of 1536: 4.2 us; with 24 elements a thread 6.7).
+// whatever it holds of the row, so a thread holds up to 32 elements and a team is 64 threads at most.
+// (fp32 rows of 2048, whose ring does not fit, are loaded directly: 113 us for 16384 rows; fewer teams
+// with a ring 126.) At 32760 rows of 1536 bf16 it takes 80 us (402 MB, 5.0 TB/s); what is left is
+// the row's dependent sums and the issue of its arithmetic by 16 warps, more than the memory.
+// Vectors in registers took 94, read per row from L1 151-250; 768 threads of 80 registers 99 (they
+// spill), every shared read before the sum that it follows 93 (likewise).
+// The register kernel: every team goes its own way, the folded vectors in its registers, for groups
+// too short to stop the CTA at (1024 elements a row, groups of 1 and 16 rows: 171 and 69 against 703
+// and 94 us; 1536, groups of 64: 92 against 87, of 256: 87 against 77), and for few rows, where latency
+// counts and more threads of one group of eight each share a row (one row of 1536: 4.2 us; with 24
+// elements a thread 6.7).
 // WIDE: a CTA of up to 512 threads for one row.
 constexpr int GRP_THREADS = 512, GRP_REGS = 128;
 constexpr int FWD_THREADS = 128;
