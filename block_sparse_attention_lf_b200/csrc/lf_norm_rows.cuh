@@ -185,12 +185,6 @@ struct Team {
     float (*red)[2][16];  // this team's [2 buffers][2 values][warps]
     int warps, warp, lane, bar, threads, phase;
 
-    __device__ __forceinline__ void sync()
-    {
-        if (warps == 1) __syncwarp();
-        else named_bar_sync(bar, threads);
-    }
-
     __device__ __forceinline__ float gather(int which)
     {
         const float4* f = reinterpret_cast<const float4*>(red[phase][which]);
@@ -403,10 +397,9 @@ __device__ __forceinline__ float normalise(Team& team, Vec8 (&t)[NV], int kind, 
     return rs;
 }
 
-// How a call's rows are taken: groups of 8 a thread (at most `most`) and threads of a team, teams of
-// a CTA, stages of the ring (as many as leave `ctas` CTAs an SM; fewer than two are not worth a ring).
+// How a call's rows are taken: threads of a team, teams of a CTA, stages of the ring (as many as leave `ctas` CTAs an SM; fewer than two are not worth a ring).
 struct NormPlan {
-    int nv, threads, teams, stages;
+    int threads, teams, stages;
     bool wide, full;
     size_t smem;
 };
@@ -417,7 +410,6 @@ NormPlan plan_of(int dim, int nv, size_t elem_bytes, int cta_threads, int ctas, 
 {
     NormPlan p;
     const int vecs = (dim + 7) / 8;
-    p.nv = nv;
     p.threads = ((vecs + nv - 1) / nv + 31) / 32 * 32;
     p.wide = p.threads > cta_threads;
     p.teams = p.wide ? 1 : std::min(MAX_TEAMS, cta_threads / p.threads);
