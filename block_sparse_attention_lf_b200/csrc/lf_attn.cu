@@ -655,8 +655,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const float mx = fmaxf(m0, m1);
             const float f0 = (n0 > 0 && m0 != -INFINITY) ? fast_exp2(m0 - mx) : 0.f;
             const float f1 = (n1 > 0 && m1 != -INFINITY) ? fast_exp2(m1 - mx) : 0.f;
+            // 0 where the row attends to nothing; NaN where a listed key or the query holds one, and then
+            // the row's output and log-sum-exp are NaN, whole or in pieces
             const float den = x.lsum[0][cc] * f0 + x.lsum[1][cc] * f1;
-            const float inv = den > 0.f ? 1.f / den : 0.f;
+            const float inv = den == 0.f ? 0.f : 1.f / den;
             x.wgt[0][cc] = f0 * inv;
             x.wgt[1][cc] = f1 * inv;
             // training: the row under the rounded weights, which sum to dent, is the row times den / dent
@@ -664,9 +666,9 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (TRAIN && a.out_lo) x.renorm[cc] = dent > 0.f ? den / dent : 1.f;
             if (slot >= 0) {
                 float* ml = a.part_ml + (static_cast<long long>(slot) * 64 + cc) * 2;
-                ml[0] = den > 0.f ? mx : -INFINITY;
-                ml[1] = den > 0.f ? den : 0.f;
-                if (TRAIN && a.out_lo) a.part_lt[static_cast<long long>(slot) * 64 + cc] = den > 0.f ? dent : 0.f;
+                ml[0] = den > 0.f ? mx : (den == 0.f ? -INFINITY : den);  // the merge leaves out -inf only
+                ml[1] = den;
+                if (TRAIN && a.out_lo) a.part_lt[static_cast<long long>(slot) * 64 + cc] = den == 0.f ? 0.f : dent;
             } else if (TRAIN && cc < q_rows) {
                 // natural log from the base-2 maximum and the fp32 denominator
                 a.lse[q_row0 + cc] = den == 0.f ? -INFINITY : (mx + log2f(den)) * 0.69314718055994531f;
@@ -789,7 +791,7 @@ __global__ void __launch_bounds__(256) attn_merge_kernel(const AttnArgs a)
         if constexpr (TRAIN) dent += __shfl_xor_sync(0xffffffffu, dent, o);
     }
     const float renorm = dent > 0.f ? den / dent : 1.f;  // as in the attention kernel's epilogue
-    const float inv = den > 0.f ? 1.f / den : 0.f;
+    const float inv = den == 0.f ? 0.f : 1.f / den;  // NaN shows, as in the attention kernel
     if (TRAIN && lane == 0) a.lse[q_row] = den == 0.f ? -INFINITY : (M + log2f(den)) * 0.69314718055994531f;
     float rest[V];  // the row under the rounded weights, less out
     uint32_t hi[V / 2];

@@ -320,7 +320,7 @@ LF_API lf_status lf_quant_fp8_rows(const uint16_t* x, int64_t n_rows, int32_t he
  *   duplicates expected); list_cap is the row stride of block_list.
  *   softmax_scale <= 0 selects 1/sqrt(head_dim).
  *   out [B,H,Lq,D] bf16: every valid query row is written; a row whose list is
- *   empty gets zeros.
+ *   empty gets zeros, one whose query or listed keys hold a NaN gets NaN.
  * Block ids outside [0, Nkv) or counts outside [0, list_cap] are skipped /
  * clamped on the device and reported as LF_ERR_LIST by lf_get_device_error().
  * Errors: LF_ERR_NULL, LF_ERR_ALIGN, LF_ERR_SHAPE, LF_ERR_CAP, LF_ERR_ARG,
@@ -438,7 +438,7 @@ LF_API lf_status lf_block_sparse_attn_fp8(const lf_hsa_shape* shape, const uint8
  *        to bf16) and normalised by their own sum, where out divides by the fp32 sum.
  *        With it a piece slot of the workspace takes 64 * (head_dim + 3) * 4 bytes.
  *   lse  [B,H,Lq] fp32: log sum_s exp(scale * <q_t, k_s>) over the row's listed
- *        tokens (natural log); -inf for a row whose list is empty.
+ *        tokens (natural log); -inf for a row whose list is empty, NaN where out is.
  * out is bit-identical to lf_block_sparse_attn_ws where the lists are split alike.
  * Two partial results over disjoint lists combine through their lse.
  * Errors: those of lf_block_sparse_attn_ws; LF_ERR_NULL / LF_ERR_ALIGN for lse.

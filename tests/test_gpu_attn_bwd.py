@@ -318,3 +318,35 @@ def test_gradient_before_a_call_is_refused():
     t = [torch.zeros(1, 1, n, 64, dtype=BF, device="cuda") for n in (64, 256, 256, 64, 64, 256, 256)]
     with pytest.raises(ValueError):
         L.HSACall(shape, 2, 1, 1, train=True).backward(*t)
+
+
+@pytest.mark.parametrize("pieces", [1, 2, 5])
+@pytest.mark.parametrize("case", [CASES[4], CASES[5]], ids=lambda c: c[0])
+def test_a_nan_shows_however_lists_are_split(case, pieces):
+    """A NaN key makes out and lse of every row that lists it NaN, a NaN query those of its own row, with the lists
+    whole or cut into pieces, in the training call and the plain one; the other rows keep their bits."""
+    shape, q, k, v, do, lists, count = _inputs(case)
+    cap, bpf, F = lists.shape[-1], shape.bpf, shape.frame_tokens
+    want = _call(shape, q, k, v, do, lists, count, tail_pieces=pieces)
+    b, h, bad = 0, 1, 3
+    k[b, h, (bad // bpf) * F + (bad % bpf) * 64] = float("nan")
+    own = next(r for r in range(shape.Rq) if int(count[b, h, r]) > 0 and bad not in lists[b, h, r, :int(count[b, h, r])])
+    row = own // bpf * F + own % bpf * 64 + 7
+    q[b, h, row] = float("nan")
+    hit = torch.zeros(q.shape[:3], dtype=torch.bool)
+    hit[b, h, row] = True
+    for r in range(shape.Rq):
+        if bad in lists[b, h, r, :int(count[b, h, r])]:
+            f, j = divmod(r, bpf)
+            hit[b, h, f * F + 64 * j:f * F + min(64 * j + 64, F)] = True
+    assert 1 < int(hit.sum()) < hit.numel()
+    out, lse, dq, _, _ = _call(shape, q, k, v, do, lists, count, tail_pieces=pieces)
+    plain, ws = torch.empty_like(out), None
+    if pieces > 1:
+        ws = torch.empty(148 * pieces * 64 * (shape.head_dim + 2) * 4, dtype=torch.uint8, device="cuda")
+    L.lf_block_sparse_attn_ws(shape, q.cuda(), k.cuda(), v.cuda(), lists.cuda(), count.cuda(), cap, 0.0, plain, ws, pieces)
+    for t in (out, plain, dq):
+        assert t.cpu()[hit].isnan().all() and torch.isfinite(t.cpu()[~hit]).all()
+    assert lse.cpu()[hit].isnan().all()
+    for t, w in ((out, want[0]), (plain, want[0]), (lse, want[1])):
+        assert torch.equal(t.cpu()[~hit], w.cpu()[~hit])
