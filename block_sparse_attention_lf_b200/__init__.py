@@ -735,7 +735,9 @@ class HSACall:
     the attention's split of the last, partial wave (0: automatic plan for the
     current device, 1: none, k >= 2: k pieces); the workspace it needs is
     allocated here. ``train=True`` keeps each row's log-sum-exp, so that
-    ``backward`` can give the gradients of the last call. ``load`` and
+    ``backward`` can give the gradients of the last call: until then its
+    q, k, v and the output it returned stay as they are, so layers whose
+    gradients are still to come have an HSACall each. ``load`` and
     ``load_bwd`` bring a chunk's fused projection into the call's tensors with
     rotary positions applied, and the gradients back.
     """
@@ -782,7 +784,7 @@ class HSACall:
         self.lse = torch.empty(s.batch, s.heads, s.Lq, dtype=f32, device=device) if train else None
         self.out_lo = torch.empty_like(self.buf.out) if train else None
         self.bwd_workspace = torch.empty(lf_attn_bwd_workspace(s), dtype=torch.uint8, device=device) if train else None
-        self.attended = False
+        self.attended = False  # out, lse and out_lo are those of the lists that the buffers hold
         # kernels enqueued per call: pool, selection (both levels), attention (+ the merge of a split)
         self.launches_per_call = 3 + (1 if ws_bytes else 0)
 
@@ -792,6 +794,7 @@ class HSACall:
 
     def select(self, stream=None):
         b = self.buf
+        self.attended = False
         lf_select_mask(self.shape, self.chunk_index, self.topk_frames, self.topk_blocks, b.q_pool, b.k_frame,
                        b.k_pool, b.frame_sel, b.block_list, b.block_count, b.list_cap, stream)
 
@@ -811,20 +814,22 @@ class HSACall:
         return [t[:, :, s.Lkv - s.Lq:s.Lkv] for t in ts]
 
     def backward(self, q, k, v, dout, dq, dk, dv, stream=None):
-        """Gradients of the last call's output in q, k and v (``train=True``; the selected blocks are constants)."""
+        """Gradients of the last call's output in q, k and v (``train=True``; the selected blocks are constants).
+        Refused where the last attention failed or lists were selected since."""
         if self.lse is None or not self.attended:
-            raise ValueError("HSACall.backward needs train=True and a call before it")
+            raise ValueError("HSACall.backward needs train=True and a call before it, with no selection in between")
         b = self.buf
         lf_block_sparse_attn_bwd(self.shape, q, k, v, b.out, dout, self.lse, b.block_list, b.block_count, b.list_cap,
                                  self.softmax_scale, dq, dk, dv, self.bwd_workspace, stream, out_lo=self.out_lo)
 
     def attend(self, q, k, v, stream=None):
         b = self.buf
-        self.attended = True
+        self.attended = False
         if self.lse is not None:
             lf_block_sparse_attn_lse(self.shape, q, k, v, b.block_list, b.block_count, b.list_cap,
                                      self.softmax_scale, b.out, self.lse, self.workspace, self.tail_pieces, stream,
                                      out_lo=self.out_lo)
+            self.attended = True
             return
         lf_block_sparse_attn_ws(self.shape, q, k, v, b.block_list, b.block_count, b.list_cap,
                                 self.softmax_scale, b.out, self.workspace, self.tail_pieces, stream)

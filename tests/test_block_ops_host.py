@@ -183,6 +183,68 @@ def test_bindings_reject_cpu_tensors():
         L.lf_rope(L.RopePlan.make(128), [x], [x], torch.zeros(4, 1, dtype=torch.int32))
 
 
+class _Steps:
+    """An HSACall on the CPU whose library calls are counted, or refused, in place of running."""
+
+    def __init__(self, monkeypatch):
+        self.refuse, self.gradients = False, 0
+        monkeypatch.setattr(L, "lf_pool", lambda *a, **k: None)
+        monkeypatch.setattr(L, "lf_select_mask", self._step)
+        monkeypatch.setattr(L, "lf_block_sparse_attn_lse", self._step)
+        monkeypatch.setattr(L, "lf_block_sparse_attn_bwd", self._gradient)
+        self.call = L.HSACall(L.LfShape.make(1, 1, 64, 64, 4, 1, 1, 1), 2, 1, 1, device="cpu", tail_pieces=1, train=True)
+
+    def _step(self, *a, **k):
+        if self.refuse:
+            raise ValueError("refused")
+
+    def _gradient(self, *a, **k):
+        self.gradients += 1
+
+    def backward(self):
+        self.call.backward(*[None] * 7)
+
+
+def test_gradient_after_a_refused_call_is_refused(monkeypatch):
+    """An attention that did not run leaves nothing to take a gradient of, neither the first one nor a later one."""
+    s = _Steps(monkeypatch)
+    s.refuse = True
+    with pytest.raises(ValueError, match="refused"):
+        s.call.attend(None, None, None)
+    with pytest.raises(ValueError, match="HSACall.backward"):
+        s.backward()
+    s.refuse = False
+    s.call(None, None, None)
+    s.backward()
+    s.backward()  # the same call's gradient of another dout
+    assert s.gradients == 2
+    s.refuse = True
+    with pytest.raises(ValueError, match="refused"):
+        s.call.attend(None, None, None)
+    with pytest.raises(ValueError, match="HSACall.backward"):
+        s.backward()
+    assert s.gradients == 2
+
+
+def test_gradient_after_another_selection_is_refused(monkeypatch):
+    """select() replaces the lists that the attention's log-sum-exp belongs to; attend() brings the two together again."""
+    s = _Steps(monkeypatch)
+    s.call(None, None, None)
+    s.call.pool(None, None)  # the pooled vectors are not the gradient's
+    s.backward()
+    s.call.select()
+    with pytest.raises(ValueError, match="HSACall.backward"):
+        s.backward()
+    s.call.attend(None, None, None)
+    s.backward()
+    s.refuse = True
+    with pytest.raises(ValueError, match="refused"):
+        s.call.select()      # it may have written some of the lists
+    with pytest.raises(ValueError, match="HSACall.backward"):
+        s.backward()
+    assert s.gradients == 2
+
+
 # ---------------------------------------------------------------- definitions against differences
 def _difference(f, inputs, grads, seed):
     """<grad, d> against (f(x + e d) - f(x - e d)) / 2 e for a random direction of every input."""
