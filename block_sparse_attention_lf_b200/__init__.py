@@ -60,7 +60,7 @@ __all__ = [
     "lf_block_sparse_attn", "lf_block_sparse_attn_ws", "lf_attn_split_plan", "lf_cag_budget",
     "lf_blocks_for_sparsity", "lf_frames_selected", "lf_list_capacity", "lf_get_device_error",
     "lf_status_string", "lf_version", "HSACall",
-    "lf_block_sparse_attn_lse", "lf_block_sparse_attn_bwd", "lf_attn_bwd_workspace",
+    "lf_block_sparse_attn_lse", "lf_attn_lse_split_plan", "lf_block_sparse_attn_bwd", "lf_attn_bwd_workspace",
     "RopePlan", "lf_rope", "NormGateShape", "lf_norm_gate", "lf_norm_gate_bwd", "lf_norm_gate_bwd_workspace",
     "ABI_FUNCTIONS", "shard_units", "shard_shape", "unit_view",
 ]
@@ -72,7 +72,7 @@ ABI_FUNCTIONS = (
     "lf_block_sparse_attn_fp8",
     "lf_block_sparse_attn", "lf_block_sparse_attn_ws", "lf_attn_split_plan", "lf_block_sparse_attn_static",
     "lf_cag_budget", "lf_blocks_for_sparsity", "lf_get_device_error", "lf_status_string", "lf_version",
-    "lf_block_sparse_attn_lse", "lf_attn_bwd_workspace", "lf_block_sparse_attn_bwd",
+    "lf_block_sparse_attn_lse", "lf_attn_lse_split_plan", "lf_attn_bwd_workspace", "lf_block_sparse_attn_bwd",
     "lf_rope_plan_init", "lf_rope", "lf_norm_gate", "lf_norm_gate_bwd_workspace", "lf_norm_gate_bwd",
 )
 
@@ -230,6 +230,8 @@ def _load() -> ctypes.CDLL:
         "lf_blocks_for_sparsity": ([F64, I32, I32, I32], I32),
         "lf_get_device_error": ([ctypes.POINTER(I32)], I32),
         "lf_block_sparse_attn_lse": ([S, P, P, P, P, P, I32, F32, P, P, P, I32, P, ctypes.c_int64, P], I32),
+        "lf_attn_lse_split_plan": ([S, I32, I32, ctypes.POINTER(I32), ctypes.POINTER(I32),
+                                   ctypes.POINTER(ctypes.c_int64)], I32),
         "lf_attn_bwd_workspace": ([S], ctypes.c_int64),
         "lf_block_sparse_attn_bwd": ([S, P, P, P, P, P, P, P, P, P, I32, F32, P, P, P, P, ctypes.c_int64, P], I32),
         "lf_rope_plan_init": ([P, I32, I32, I32, I32, P, F64, I32, F64, F64, F64, F64], I32),
@@ -520,7 +522,8 @@ def _attn_args(shape: LfShape, dev: int, q, k, v, block_list, block_count, list_
 def lf_block_sparse_attn_lse(shape: LfShape, q, k, v, block_list, block_count, list_cap: int, softmax_scale: float,
                              out, lse, workspace=None, tail_pieces: int = 0, stream=None, out_lo=None) -> None:
     """lf_block_sparse_attn_ws that also writes each row's log-sum-exp (fp32 [B,H,Lq]; -inf for an empty list)
-    and, for the gradient, ``out_lo`` (like out): out + out_lo is the row under the rounded softmax weights."""
+    and, for the gradient, ``out_lo`` (like out): out + out_lo is the row under the rounded softmax weights. With
+    ``out_lo`` the workspace of the automatic split is lf_attn_lse_split_plan's."""
     import torch
     dev = _device()
     qp, kp, vp, lp, cp = _attn_args(shape, dev, q, k, v, block_list, block_count, list_cap)
@@ -686,9 +689,18 @@ def lf_norm_gate_bwd(shape: NormGateShape, x, y, dr, dh, dx, dy, grads: dict, wo
 
 def lf_attn_split_plan(shape: LfShape, list_cap: int, sm: int = 0) -> Tuple[int, int, int]:
     """(tail query blocks, pieces per list, workspace bytes) of the automatic split."""
+    return _split_plan("lf_attn_split_plan", shape, list_cap, sm)
+
+
+def lf_attn_lse_split_plan(shape: LfShape, list_cap: int, sm: int = 0) -> Tuple[int, int, int]:
+    """lf_attn_split_plan for lf_block_sparse_attn_lse with out_lo, whose piece slots are larger."""
+    return _split_plan("lf_attn_lse_split_plan", shape, list_cap, sm)
+
+
+def _split_plan(name: str, shape: LfShape, list_cap: int, sm: int) -> Tuple[int, int, int]:
     t, p, b = ctypes.c_int32(0), ctypes.c_int32(0), ctypes.c_int64(0)
-    _check(_lib.lf_attn_split_plan(ctypes.byref(shape), list_cap, sm, ctypes.byref(t), ctypes.byref(p),
-                                   ctypes.byref(b)), "lf_attn_split_plan")
+    _check(getattr(_lib, name)(ctypes.byref(shape), list_cap, sm, ctypes.byref(t), ctypes.byref(p),
+                               ctypes.byref(b)), name)
     return t.value, p.value, b.value
 
 

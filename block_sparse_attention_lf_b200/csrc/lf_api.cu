@@ -98,8 +98,9 @@ int blocks_per_frame(const Derived& d, int chunk_index, int topk_blocks)
 lf_status launch_status(cudaError_t e) { return e == cudaSuccess ? LF_OK : LF_ERR_CUDA; }
 
 // Bytes of one partial-result slot of the attention split: 64 rows of head_dim
-// fp32 values plus a (max, denominator) pair per row.
-long long split_slot_bytes(int D) { return 64ll * (D + 2) * 4; }
+// fp32 values plus a (max, denominator) pair per row and, for out_lo, the sum of
+// the rounded weights.
+long long split_slot_bytes(int D, bool out_lo = false) { return 64ll * (D + (out_lo ? 3 : 2)) * 4; }
 
 // Split of the last, partial wave of the one-CTA-per-query-block attention.
 // With n_rows query blocks on sm SMs, the last r = n_rows mod sm query blocks
@@ -453,8 +454,10 @@ lf_status lf_select_frames_ivf(const lf_hsa_shape* shape, int32_t chunk_index, i
     return launch_status(lf::launch_select_frames_ivf(a, static_cast<cudaStream_t>(stream)));
 }
 
-lf_status lf_attn_split_plan(const lf_hsa_shape* shape, int32_t list_cap, int32_t sm, int32_t* tail_rows,
-                             int32_t* pieces, int64_t* workspace_bytes)
+namespace {
+
+lf_status plan_split(const lf_hsa_shape* shape, int32_t list_cap, int32_t sm, bool out_lo, int32_t* tail_rows,
+                     int32_t* pieces, int64_t* workspace_bytes)
 {
     Derived d;
     lf_status st = check_shape(shape, &d);
@@ -466,8 +469,22 @@ lf_status lf_attn_split_plan(const lf_hsa_shape* shape, int32_t list_cap, int32_
     split_plan(static_cast<long long>(d.B) * d.H * d.Rq, sm, list_cap, 0, -1, &t, &kp);
     *tail_rows = t;
     *pieces = kp;
-    *workspace_bytes = static_cast<int64_t>(t) * kp * split_slot_bytes(d.D);
+    *workspace_bytes = static_cast<int64_t>(t) * kp * split_slot_bytes(d.D, out_lo);
     return LF_OK;
+}
+
+}  // namespace
+
+lf_status lf_attn_split_plan(const lf_hsa_shape* shape, int32_t list_cap, int32_t sm, int32_t* tail_rows,
+                             int32_t* pieces, int64_t* workspace_bytes)
+{
+    return plan_split(shape, list_cap, sm, false, tail_rows, pieces, workspace_bytes);
+}
+
+lf_status lf_attn_lse_split_plan(const lf_hsa_shape* shape, int32_t list_cap, int32_t sm, int32_t* tail_rows,
+                                 int32_t* pieces, int64_t* workspace_bytes)
+{
+    return plan_split(shape, list_cap, sm, true, tail_rows, pieces, workspace_bytes);
 }
 
 lf_status lf_block_sparse_attn(const lf_hsa_shape* shape, const uint16_t* q, const uint16_t* k, const uint16_t* v,
@@ -607,8 +624,7 @@ lf_status attn_bf16(const lf_hsa_shape* shape, const uint16_t* q, const uint16_t
     if (workspace_bytes > 0 && tail_pieces != 1) {
         int sm = 0;
         if ((st = sm_count(&sm)) != LF_OK) return st;
-        split_plan(n_rows, sm, list_cap, tail_pieces, workspace_bytes / (split_slot_bytes(d.D) + (out_lo ? 64 * 4 : 0)),
-                   &tail, &pieces);
+        split_plan(n_rows, sm, list_cap, tail_pieces, workspace_bytes / split_slot_bytes(d.D, out_lo), &tail, &pieces);
     }
     float* part_o = static_cast<float*>(workspace);
     float* part_ml = pieces ? part_o + static_cast<long long>(tail) * pieces * 64 * d.D : nullptr;

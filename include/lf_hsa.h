@@ -30,6 +30,7 @@
  *   lf_quant_fp8_rows    per-token e4m3 codes and scales (the FP8 attention's q, k)
  *   lf_block_sparse_attn_fp8  the attention with e4m3 q and k (tcgen05 kind::f8f6f4)
  *   lf_block_sparse_attn_lse  the attention with each row's log-sum-exp (training)
+ *   lf_attn_lse_split_plan    its split's plan and workspace size (host only)
  *   lf_block_sparse_attn_bwd  its gradient in q, k and v over the same lists
  *   lf_attn_bwd_workspace     the gradient's workspace size (host only)
  *
@@ -436,7 +437,9 @@ LF_API lf_status lf_block_sparse_attn_fp8(const lf_hsa_shape* shape, const uint8
  *   out_lo  [B,H,Lq,D] bf16, for the gradient; NULL: not wanted. out + out_lo is, to
  *        2^-16, the row under the softmax weights as the tensor cores use them (rounded
  *        to bf16) and normalised by their own sum, where out divides by the fp32 sum.
- *        With it a piece slot of the workspace takes 64 * (head_dim + 3) * 4 bytes.
+ *        With it a piece slot of the workspace takes 64 * (head_dim + 3) * 4 bytes
+ *        (lf_attn_lse_split_plan), so a workspace of lf_attn_split_plan's size gives
+ *        fewer pieces.
  *   lse  [B,H,Lq] fp32: log sum_s exp(scale * <q_t, k_s>) over the row's listed
  *        tokens (natural log); -inf for a row whose list is empty, NaN where out is.
  * out is bit-identical to lf_block_sparse_attn_ws where the lists are split alike.
@@ -447,6 +450,14 @@ LF_API lf_status lf_block_sparse_attn_lse(const lf_hsa_shape* shape, const uint1
                                    const uint16_t* v, const int32_t* block_list, const int32_t* block_count,
                                    int32_t list_cap, float softmax_scale, uint16_t* out, uint16_t* out_lo,
                                    float* lse, int32_t tail_pieces, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * lf_attn_split_plan for lf_block_sparse_attn_lse with out_lo: the same plan, host only.
+ *   workspace_bytes out  tail_rows * pieces * 64 * (head_dim + 3) * 4
+ * Errors: those of lf_attn_split_plan.
+ */
+LF_API lf_status lf_attn_lse_split_plan(const lf_hsa_shape* shape, int32_t list_cap, int32_t sm,
+                                 int32_t* tail_rows, int32_t* pieces, int64_t* workspace_bytes);
 
 /* Workspace bytes of lf_block_sparse_attn_bwd for a shape (host only); -1 on a bad shape. */
 LF_API int64_t lf_attn_bwd_workspace(const lf_hsa_shape* shape);

@@ -177,6 +177,28 @@ def test_attn_grad_refusals():
         L.lf_attn_bwd_workspace(L.LfShape.make(1, 2, 96, 1560, 21, 1, 1, 3))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,H,nc,kb,sm", [(1, 12, 3, 12, 148), (1, 2, 3, 12, 148), (1, 1, 1, 12, 148), (1, 12, 3, 1, 148),
+                                          (1, 4, 37, 12, 148), (1, 12, 3, 12, 132), (1, 24, 3, 12, 148)])
+def test_training_split_plan(B, H, nc, kb, sm, D):
+    """The plain call's plan, with the slots that out_lo's sums need."""
+    sh = L.LfShape.make(B, H, D, 1560, 18 + nc, 1, 1, nc)
+    cap = L.lf_list_capacity(sh, 2, 4, kb)
+    t, k, nbytes = L.lf_attn_lse_split_plan(sh, cap, sm)
+    assert (t, k) == L.lf_attn_split_plan(sh, cap, sm)[:2]
+    assert nbytes == t * k * 64 * (D + 3) * 4
+
+
+def test_training_split_plan_refusals():
+    sh, f = L.LfShape.make(1, 2, 128, 1560, 21, 1, 1, 3), L.lib.lf_attn_lse_split_plan
+    t, k, b = (ctypes.byref(c()) for c in (ctypes.c_int32, ctypes.c_int32, ctypes.c_int64))
+    assert f(None, 108, 148, t, k, b) == 1 and f(ctypes.byref(sh), -1, 148, t, k, b) == 5
+    for args in ((None, k, b), (t, None, b), (t, k, None)):
+        assert f(ctypes.byref(sh), 108, 148, *args) == 1
+    with pytest.raises(L.LfError):
+        L.lf_attn_lse_split_plan(L.LfShape.make(1, 2, 96, 1560, 21, 1, 1, 3), 108, 148)
+
+
 def test_bindings_reject_cpu_tensors():
     x = torch.zeros(1, 2, 4, 128)
     with pytest.raises((ValueError, RuntimeError, AssertionError)):

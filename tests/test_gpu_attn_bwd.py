@@ -350,3 +350,25 @@ def test_a_nan_shows_however_lists_are_split(case, pieces):
     assert lse.cpu()[hit].isnan().all()
     for t, w in ((out, want[0]), (plain, want[0]), (lse, want[1])):
         assert torch.equal(t.cpu()[~hit], w.cpu()[~hit])
+
+
+def test_planned_workspace_gives_the_planned_pieces():
+    """A training call with a workspace of exactly the planned size is cut as the plain call with its own, so out keeps
+    its bits; with the plain call's size it would be a piece short."""
+    shape = L.LfShape.make(1, 1, 128, 320, 8, 1, 1, 2)
+    g = torch.Generator().manual_seed(47)
+    q = torch.randn(1, 1, 640, 128, generator=g).to(BF).cuda()
+    k, v = (torch.randn(1, 1, 8 * 320, 128, generator=g).to(BF).cuda() for _ in range(2))
+    lists, count = (t.cuda() for t in _lists(g, 1, 1, shape.Rq, shape.Nkv, 30, "full"))
+    outs = []
+    for plan in (L.lf_attn_split_plan, L.lf_attn_lse_split_plan):
+        tail, pieces, nbytes = plan(shape, 30)
+        assert (tail, pieces) == (10, 3)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        outs.append(torch.empty_like(q))
+        if plan is L.lf_attn_split_plan:
+            L.lf_block_sparse_attn_ws(shape, q, k, v, lists, count, 30, 0.0, outs[-1], ws)
+        else:
+            L.lf_block_sparse_attn_lse(shape, q, k, v, lists, count, 30, 0.0, outs[-1],
+                                       torch.empty(1, 1, 640, device="cuda"), ws, out_lo=torch.empty_like(q))
+    assert torch.equal(*outs)
