@@ -372,3 +372,37 @@ def test_planned_workspace_gives_the_planned_pieces():
             L.lf_block_sparse_attn_lse(shape, q, k, v, lists, count, 30, 0.0, outs[-1],
                                        torch.empty(1, 1, 640, device="cuda"), ws, out_lo=torch.empty_like(q))
     assert torch.equal(*outs)
+
+
+LONG_LISTS = [
+    # name, B, H, D, F, frames, sink, recent, cur, list length, counts
+    # more query blocks list a KV block than two 32-entry windows of its list hold, an odd number of them
+    ("key_lists_d128", 1, 2, 128, 33, 73, 1, 1, 71, 73, "full", 1.0, 0),
+    ("key_lists_d64", 1, 2, 64, 33, 73, 1, 1, 71, 73, "full", 1.0, 0),
+    ("uneven_key_lists", 2, 1, 128, 70, 52, 1, 1, 50, 104, "ragged", 1.0, 0),   # two blocks a frame, one of six tokens
+    # more query blocks than the transposition takes at once (256)
+    ("many_query_blocks", 1, 2, 128, 3, 320, 6, 4, 300, 90, "ragged", 1.0, 0),
+    ("three_sweeps_d64", 1, 1, 64, 2, 606, 4, 2, 600, 120, "ragged", 1.0, 0),
+]
+
+
+@pytest.mark.parametrize("case", LONG_LISTS, ids=[c[0] for c in LONG_LISTS])
+def test_long_key_lists(case):
+    """Key items of many tiles, whose list ids and row statistics are fetched anew every 32 entries, and transpositions
+    of more than one sweep."""
+    shape, q, k, v, do, lists, count = _inputs(case)
+    listed = torch.zeros(shape.batch * shape.heads, shape.Nkv, dtype=torch.int64)
+    flat, n = lists.reshape(-1, shape.Rq, lists.shape[-1]).long(), count.reshape(-1, shape.Rq, 1)
+    for u in range(flat.shape[0]):
+        listed[u] = torch.bincount(flat[u][torch.arange(flat.shape[-1]) < n[u]], minlength=shape.Nkv)
+    if case[10] == "full":
+        assert (listed == shape.Rq).all() and shape.Rq == 71
+    elif shape.Rq > 256:
+        assert shape.Rq > 256 and int(listed.max()) > 64
+    else:
+        assert int((listed > 32).sum()) > 50 and len(listed.unique()) > 10
+    got = _call(shape, q, k, v, do, lists, count)
+    _check(shape, q, k, v, do, lists, count, 0.0, got)
+    assert L.lf_get_device_error() == (0, 0)
+    again = _call(shape, q, k, v, do, lists, count)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
