@@ -173,3 +173,37 @@ def test_rope_stream_and_graph():
     graph.replay()
     L.lf_rope(plan, [x], [want], pos)
     assert torch.equal(out, want) and math.isfinite(float(out.float().sum()))
+
+
+MANY = [
+    # B, heads of the tensors, T, D, rot, layout, dtype, odd (elements a head is apart beyond D), what it runs
+    (1, (5, 3, 4), 19009, 128, 128, "half", "bf16", 0),          # a thread takes all twelve heads of three tensors
+    (1, (5, 3, 4), 4001, 128, 128, "interleaved", "bf16", 0),    # four heads a thread: one meets two tensors
+    (2, (7, 1), 6001, 64, 64, "half", "fp16", 0),                # a tensor of one head behind one of seven
+    (1, (4,), 12001, 128, 64, "half", "fp32", 0),                # three heads asked for, then one; half of each copied
+    (1, (2, 1, 1), 5003, 128, 128, "interleaved", "fp32", 0),
+    (1, (3, 2), 9001, 66, 66, "interleaved", "bf16", 1),         # single elements: a pair is two loads
+]
+
+
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("case", MANY)
+def test_rope_threads_of_several_heads(case, backward):
+    """So many tokens that a thread takes several heads: later heads are asked for before earlier ones are stored,
+    across the tensors of a call, into other tensors and in place."""
+    B, heads, n, D, rot, layout, dt, odd = case
+    rows = 1 if odd else (8 if dt == "fp16" or dt == "bf16" else 4)
+    spans = (rot // 2 if layout == "half" else rot // (2 if odd else 1)) // rows + (D - rot) // rows
+    want = -(-148 * 1024 // (B * n * spans))                     # groups of heads the launch asks for
+    assert -(-sum(heads) // min(want, sum(heads))) >= 2          # heads a thread takes
+    g = torch.Generator().manual_seed(n + D)
+    wide = [torch.randn(B, h, n, D + odd, generator=g).to(T[dt]).cuda() for h in heads]
+    xs = [t[..., :D] for t in wide]
+    pos = torch.randint(-3000, 90000, (n, 1), generator=g)
+    plan, f = L.RopePlan.make(D, rot, layout), R.rope_frequencies((rot,), 10000.0)
+    rotate = (True, True, False)[:len(heads)] if len(heads) > 1 else (True,)
+    outs = [torch.full((B, h, n, D), 7.0, dtype=T[dt], device="cuda") for h in heads]
+    L.lf_rope(plan, xs, outs, pos.int().cuda(), rotate, backward)
+    _check(plan, f, xs, pos, layout, rot, rotate, backward, outs)
+    L.lf_rope(plan, xs, xs, pos.int().cuda(), rotate, backward)
+    assert all(torch.equal(x, o) for x, o in zip(xs, outs))
