@@ -303,3 +303,163 @@ def test_graph_and_stream():
         t.zero_()
     graph.replay()
     assert all(torch.equal(t, w) for t, w in zip(out + list(grads.values()), want))
+
+
+# ---------------------------------------------------------------- many rows a team
+def _terms(shape, x, y, dr, dh, v):
+    """In 64 bits: (r, h, dx, dy, what each row adds to each vector's gradient), and for dx and dy the size of the
+    terms that their last subtraction takes apart. Written from the formulas of the gradient, not by autograd."""
+    f = lambda t: None if t is None else t.double()  # noqa: E731
+    per, alpha, eps = shape.rows_per_group, float(shape.residual_scale), float(shape.eps)
+    at = torch.arange(shape.rows, device=x.device) // per
+    one, zero = torch.ones((), dtype=torch.float64, device=x.device), torch.zeros((), dtype=torch.float64, device=x.device)
+    vec = {n: f(v[n]) if n in v else (zero if n in ("shift", "scale") or n.endswith("b") else one) for n in NAMES}
+    gate, scale, shift = (vec[n][at] if n in v else vec[n] for n in NAMES[:3])
+    w1, b1, w2, b2 = (vec[n] for n in NAMES[3:])
+    x, y, dr, dh = f(x), f(y), f(dr), f(dh)
+
+    def hat(t, kind):
+        if kind == 0:
+            return t, 1.0
+        t = t - t.mean(-1, keepdim=True) if kind == 2 else t
+        rs = torch.rsqrt(t.square().mean(-1, keepdim=True) + eps)
+        return t * rs, rs
+
+    def back(d, n, rs, kind):
+        if kind == 0:
+            return d, d.abs()
+        size = rs * (d.abs() + n.abs() * (d * n).abs().mean(-1, keepdim=True))
+        out = d - n * (d * n).mean(-1, keepdim=True)
+        if kind == 2:
+            out, size = out - d.mean(-1, keepdim=True), size + rs * d.abs().mean(-1, keepdim=True)
+        return rs * out, size
+
+    m, rs2 = hat(y, shape.post_norm)
+    u = m * w2 + b2
+    r = alpha * x + gate * u
+    n, rs1 = hat(r, shape.pre_norm)
+    a = n * w1 + b1
+    d, s1 = back(dh * (1 + scale) * w1, n, rs1, shape.pre_norm)
+    d, s1 = d + dr, s1 + dr.abs()
+    dy, s2 = back(d * gate * w2, m, rs2, shape.post_norm)
+    s2 = s2 + (rs2 * (gate * w2).abs() * s1 if shape.post_norm else (gate * w2).abs() * s1)
+    terms = {"gate": d * u, "scale": dh * a, "shift": dh, "pre_w": dh * (1 + scale) * n, "pre_b": dh * (1 + scale),
+             "post_w": d * gate * m, "post_b": d * gate}
+    return r, a * (1 + scale) + shift, (alpha * d, abs(alpha) * s1), (dy, s2), {k: t.expand_as(x) for k, t in terms.items()}
+
+
+def _sums(t, name, shape):
+    """Sums over a group's rows, or over all."""
+    if name not in NAMES[:3]:
+        return t.sum(0)
+    pad = torch.zeros(shape.groups * shape.rows_per_group - shape.rows, shape.dim, dtype=t.dtype, device=t.device)
+    return torch.cat([t, pad]).view(shape.groups, shape.rows_per_group, shape.dim).sum(1)
+
+
+MANY = [
+    # the group kernel, threads with every column of a row: eight rows a team over a ring of four
+    (9001, 1536, 1560, "bf16", "bf16", "layer", "layer", " ".join(NAMES)),
+    (7000, 1536, 3000, "fp32", "bf16", "rms", "rms", "gate scale shift pre_w post_w"),
+    (12000, 512, 700, "bf16", "bf16", "layer", "none", "gate scale shift"),
+    (6000, 768, 97, "fp16", "fp16", "rms", "layer", " ".join(NAMES)),      # threads past the row's end
+    (3000, 2048, 400, "fp32", "fp32", "layer", "rms", " ".join(NAMES)),    # no ring forward
+    (6001, 1333, 500, "bf16", "bf16", "rms", "none", "gate scale"),        # odd: loaded directly
+    # the register kernel: every team its own groups
+    (20000, 1024, 16, "bf16", "bf16", "layer", "rms", "gate scale shift"),
+    (9000, 512, 1, "bf16", "bf16", "layer", "none", "gate scale shift"),
+    (12003, 256, 50, "fp32", "fp16", "rms", "rms", " ".join(NAMES)),
+    # rows of a CTA each
+    (1500, 4096, 200, "bf16", "bf16", "layer", "layer", " ".join(NAMES)),
+    (1300, 5120, 1300, "fp32", "bf16", "rms", "rms", "gate scale shift pre_w post_w"),
+    (1200, 8192, 64, "fp16", "fp16", "layer", "none", "gate scale shift"),
+    (900, 12288, 300, "bf16", "bf16", "rms", "layer", " ".join(NAMES)),
+    (800, 16384, 100, "fp32", "fp32", "layer", "rms", " ".join(NAMES)),
+    (1000, 2600, 7, "bf16", "bf16", "layer", "layer", "gate scale shift post_b"),
+    (700, 4099, 150, "fp32", "bf16", "rms", "none", "gate scale"),
+]
+
+
+@pytest.mark.parametrize("case", MANY)
+def test_many_rows_a_team(case):
+    """Rings whose stages are used again and again, several groups a CTA, and gradients of vectors held row by row."""
+    shape, *ts, v = _inputs(case, 7)
+    x, y, dr, dh = (t.cuda() for t in ts)
+    vd = {n: t.cuda() for n, t in v.items()}
+    r, h, dx, dy = torch.empty_like(x), torch.empty_like(y), torch.empty_like(x), torch.empty_like(y)
+    grads = {n: torch.full_like(t, 9.0) for n, t in vd.items()}
+    ws = torch.full((L.lf_norm_gate_bwd_workspace(shape),), 255, dtype=torch.uint8, device="cuda")
+    L.lf_norm_gate(shape, x, y, r, h, **vd)
+    L.lf_norm_gate_bwd(shape, x, y, dr, dh, dx, dy, grads, ws, **vd)
+    rr, hh, (dxr, _), (dyr, _), terms = _terms(shape, x, y, dr, dh, vd)
+    for got, ref, steps, what in ((r, rr, 1, "r"), (h, hh, 2, "h"), (dx, dxr, 3, "dx"), (dy, dyr, 3, "dy")):
+        _close(got, ref.cpu(), got.dtype, steps, what)
+    _hold_vectors(shape, grads, terms)
+    # in place, and the same bits
+    again = {n: torch.empty_like(t) for n, t in grads.items()}
+    L.lf_norm_gate_bwd(shape, x, y, dr, dh, dr, dh, again, ws, **vd)
+    assert torch.equal(dr, dx) and torch.equal(dh, dy) and all(torch.equal(again[n], t) for n, t in grads.items())
+    L.lf_norm_gate(shape, x, y, x, y, **vd)
+    assert torch.equal(x, r) and torch.equal(y, h)
+
+
+def _hold_vectors(shape, grads, terms):
+    """A row's term is within three chained row sums (as dx is, _close); a column adds at most its rows, or the rows
+    of a CTA and then 148 CTAs' partial sums by 32 threads, one after another, 2^-24 of the terms' sizes each; and two
+    products. In norm: the terms' errors add up as the terms do."""
+    for n, got in grads.items():
+        t, got = terms[n], got.double()
+        ref, size = _sums(t, n, shape), _sums(t.abs(), n, shape)
+        rms = _sums(t.square().mean(-1, keepdim=True).sqrt().expand_as(t), n, shape)
+        chain = min(shape.rows_per_group if n in NAMES[:3] else shape.rows, -(-shape.rows // 148) + 148) + 4
+        bound = 3 * SUM * 8 * torch.maximum(rms, size) + chain * 2.0 ** -24 * size
+        worst = float(((got - ref).abs() - bound).max())
+        assert torch.isfinite(got).all() and worst <= 0, (n, worst)
+        off = float((got - ref).norm() / ref.norm().clamp_min(1e-30))
+        assert off <= 3 * SUM + chain * 2.0 ** -24, (n, off)
+
+
+TIGHT = [c for c in CASES if c[1] > 3] + [
+    (2001, 256, 1, "bf16", "bf16", "rms", "layer", " ".join(NAMES)),
+]
+
+
+@pytest.mark.parametrize("case", TIGHT)
+def test_vector_gradients_row_by_row(case):
+    """The gradients of gate, scale, shift, weights and biases within what their own group's rows allow."""
+    shape, *ts, v = _inputs(case, 8)
+    x, y, dr, dh = (t.cuda() for t in ts)
+    vd = {n: t.cuda() for n, t in v.items()}
+    grads = {n: torch.full_like(t, 9.0) for n, t in vd.items()}
+    ws = torch.empty(L.lf_norm_gate_bwd_workspace(shape), dtype=torch.uint8, device="cuda")
+    L.lf_norm_gate_bwd(shape, x, y, dr, dh, None, None, grads, ws, **vd)
+    _hold_vectors(shape, grads, _terms(shape, x, y, dr, dh, vd)[4])
+
+
+@pytest.mark.parametrize("dim", [1, 2, 3])
+@pytest.mark.parametrize("pre,post", [("rms", "rms"), ("layer", "rms"), ("rms", "layer"), ("layer", "none")])
+@pytest.mark.parametrize("types", [("fp32", "fp32"), ("bf16", "bf16"), ("fp32", "fp16")])
+def test_rows_of_few_elements(dim, pre, post, types):
+    """Rows of one to three elements, with eps = 1 so that no norm divides by almost nothing: half a step, and three
+    chained statistics of the terms that the gradient's subtractions take apart. A statistic is off by 2^-24 for each
+    of its sum's dim terms (zeros add no error), four for 2 ulp of 1 / deviation, three for eps, the mean and the
+    product; 1 / deviation is at most 1, and a row's values, of size `big`, move it by as much at most."""
+    case = (45, dim, 9, *types, pre, post, "gate scale shift pre_w" + (" post_w post_b" if post != "none" else ""))
+    _, *ts, v = _inputs(case, 9)
+    shape = L.NormGateShape.make(45, dim, 9, T[types[0]], T[types[1]], pre, post, 1.0, 0.75)
+    x, y, dr, dh = (t.cuda() for t in ts)
+    vd = {n: t.cuda() for n, t in v.items()}
+    r, h, dx, dy = torch.empty_like(x), torch.empty_like(y), torch.empty_like(x), torch.empty_like(y)
+    grads = {n: torch.full_like(t, 9.0) for n, t in vd.items()}
+    ws = torch.empty(L.lf_norm_gate_bwd_workspace(shape), dtype=torch.uint8, device="cuda")
+    L.lf_norm_gate(shape, x, y, r, h, **vd)
+    L.lf_norm_gate_bwd(shape, x, y, dr, dh, dx, dy, grads, ws, **vd)
+    rr, hh, *sized, terms = _terms(shape, x, y, dr, dh, vd)
+    big, few = max(float(t.abs().max()) for t in (x, y)), 3 * (dim + 7) * 2.0 ** -24
+    for got, (ref, size) in zip((r, h, dx, dy), ((rr, big * (1 + rr.abs())), (hh, big * (1 + hh.abs())), *sized)):
+        tiny = 2.0 ** -25 if got.dtype == torch.float16 else 0.0
+        bound = R.EPS[got.dtype] * ref.abs() + few * (1 + big) * size + tiny
+        err = (got.double() - ref).abs()
+        assert (err <= bound).all(), float((err - bound).max())
+    for n, t in grads.items():
+        size = _sums(terms[n].abs(), n, shape) + _sums(torch.ones_like(terms[n]), n, shape)
+        assert ((t.double() - _sums(terms[n], n, shape)).abs() <= few * (1 + big) * size).all(), n
