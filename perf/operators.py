@@ -250,7 +250,8 @@ def _own_attn(s):
     c = s["case"]
     if "shape" not in s:
         s["shape"] = lf.LfShape.make(c["B"], c["H"], c["D"], c["F"], c["frames"], c["sink"], c["recent"], c["cur"])
-        fwd = lf.lf_attn_lse_split_plan(s["shape"], s["cap"])[2]
+        tail, pieces, _ = lf.lf_attn_split_plan(s["shape"], s["cap"])
+        fwd = tail * pieces * 64 * (c["D"] + 3) * 4  # a piece's slot in a training call
         s["ws"] = torch.empty(fwd, dtype=torch.uint8, device="cuda") if fwd else None
         s["out_lo"] = torch.empty_like(s["out"])
         s["ws_bwd"] = torch.empty(lf.lf_attn_bwd_workspace(s["shape"]), dtype=torch.uint8, device="cuda")
