@@ -44,12 +44,15 @@
 // Every wait is bounded, as in the forward kernel.
 //
 // Measured at layer480p (12 heads of 4680 queries, 21 frames of 1560 tokens, head_dim 128, 108 blocks a
-// row): preparing kernel 20 us, this one 767 us (query items 262, key items 505), 884 TFLOP/s for its
-// seven products. A key item's tile takes about 2360 cycles, of which its MMAs are 1536 (M = 128, N = 64
-// products are bound by their operands' shared-memory bandwidth); two slots of a ring, which is what
-// shared memory holds beside the own blocks, do not hide the rest of the chain load - scores -
-// softmax - products. Tried and left: S' and dP' on barriers of their own, a third Xs tile for key
-// items in place of the second own block, dk before dv (each slower or within 20 us).
+// row; 1965 MHz): preparing kernel 20 us, this one 767 us, 884 TFLOP/s for its seven products; query
+// items alone 308 us, key items alone 509. A key item's tile takes about 2950 cycles, boundaries among
+// them, of which its MMAs are 1536 (M = 128, N = 64 products are bound by their operands' shared-memory
+// bandwidth). A clock around every wait: the score warp stands 1084 cycles a key tile for Ys and 324 for
+// Xs, the accumulating warp 1147 for P and dS, the softmax 828 for scores; a query tile of about 1840
+// has 364 and 559 of the first and third. So two slots of a ring, which is what shared memory holds
+// beside the own blocks, do not hide a key tile's chain load - scores - softmax - products (without the
+// exponentials it still takes 495 us). Tried and left: S' and dP' on barriers of their own, a third Xs
+// tile for key items in place of the second own block, dk before dv (each slower or within 20 us).
 #include "lf_attn_bwd.h"
 #include "lf_internal.h"
 #include "lf_device.cuh"

@@ -51,7 +51,8 @@ namespace {
 // and 94 us; 1536, groups of 64: 92 against 87, of 256: 87 against 77), and for few rows, where latency
 // counts and more threads of one group of eight each share a row (one row of 1536: 4.2 us; with 24
 // elements a thread 6.7).
-// WIDE: a CTA of up to 512 threads for one row.
+// WIDE: a CTA of up to 512 threads for one row (4096: 105 us for 8192 rows, 2.6 TB/s; above 8192 its
+// four groups a thread spill, 656 / 388 bytes and more: 118 us for 2048 rows of 16384).
 constexpr int GRP_THREADS = 512, GRP_REGS = 128;
 constexpr int FWD_THREADS = 128;
 template <int NV, bool WIDE> constexpr int FWD_REGS = !WIDE && NV == 1 ? 80 : 128;

@@ -9,9 +9,15 @@ namespace {
 // One CTA an SM, so that few partial sums are written: 384 threads that hold two groups of eight
 // (32760 rows of 1536 bf16, 604 MB: 202 us, 3.0 TB/s; one group in 192 threads 284, three in 64
 // threads 266). What the row's first halves need is read before the sums that precede its use, as far
-// as registers last (208 without; with every read so, 337: it spills). The bound is a row's chain of four dependent sums and the issue of its arithmetic by
-// twelve warps; more warps would leave the column sums no registers. WIDE:
-// longer rows take up to 512 threads, of two groups to 8192 and of four above.
+// as registers last (208 without; with every read so, 337: it spills). The bound is a row's chain of
+// four dependent sums and the issue of its arithmetic by twelve warps; more warps would leave the column
+// sums no registers. Rows that leave threads of a team idle spill where the post norm has a bias (460 /
+// 792 bytes a thread stored and loaded; 768 wide: 298 us for 32760 rows).
+// WIDE: longer rows take up to 512 threads, of two groups to 8192 and of four above. Their column sums,
+// 64 and 128 registers of 128, spill (bf16: 424 / 636 to 3172 / 4064 bytes), and one row an SM is at
+// work: 8192 rows of 4096 take 499 us, 2048 of 16384 564, where 16384 of 2048 take 145.
+// Short groups are dear whatever the width: each stops its CTA and leaves four fp32 partial rows (32760
+// rows of 1536 in groups of 16: 185 us and the finish 309; of one: 1227 and 4183).
 template <bool WIDE> constexpr int BWD_REGS = WIDE ? 128 : 168;
 constexpr int BWD_THREADS = 384;
 

@@ -619,7 +619,8 @@ typedef struct lf_norm_gate_vectors {
 LF_API lf_status lf_norm_gate(const lf_norm_gate_shape* shape, const lf_norm_gate_vectors* vectors, const void* x,
                        const void* y, void* r, void* h, void* stream);
 
-/* Workspace bytes of lf_norm_gate_bwd (host only); -1 on a bad shape. */
+/* Workspace bytes of lf_norm_gate_bwd (host only); -1 on a bad shape. It grows with the
+ * number of groups, by 16 bytes an element of a row each. */
 LF_API int64_t lf_norm_gate_bwd_workspace(const lf_norm_gate_shape* shape);
 
 /*
